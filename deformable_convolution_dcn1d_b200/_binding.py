@@ -11,6 +11,7 @@ import contextlib
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -24,7 +25,10 @@ _P = ctypes.c_void_p
 DCN1D_F32 = 0
 DCN1D_BF16 = 1
 DCN1D_F16 = 2
-_DTYPES = {torch.float32: DCN1D_F32, torch.bfloat16: DCN1D_BF16, torch.float16: DCN1D_F16}
+DCN1D_I8 = 3
+DCN1D_U8 = 4
+_DTYPES = {torch.float32: DCN1D_F32, torch.bfloat16: DCN1D_BF16, torch.float16: DCN1D_F16,
+           torch.int8: DCN1D_I8, torch.uint8: DCN1D_U8}
 _BAD_DTYPE = 99   # any other torch dtype: the library rejects it with DCN1D_ERR_DTYPE
 
 STATUS = {0: "DCN1D_OK", 1: "DCN1D_ERR_NULL", 2: "DCN1D_ERR_DTYPE", 3: "DCN1D_ERR_SHAPE",
@@ -92,6 +96,15 @@ SIGNATURES = [
      [_T, _T, _T, _T, _T] + [_I64] * 6 + [_INT] + [_T] * 5),
     ("dcn1d_test_forward_stalled", _INT,
      [_T, _T, _T, _I64, _I64, _I64, _I64, _I64, _INT, _T, _I64, _P]),
+    ("dcn1d_layer_norm_forward", _INT, [_T] * 3 + [ctypes.c_float] + [_T] * 5 + [_P]),
+    ("dcn1d_layer_norm_backward_workspace_size", _I64, [_T] * 10),
+    ("dcn1d_layer_norm_backward", _INT, [_T] * 10 + [_P, ctypes.c_size_t, _P]),
+    ("dcn1d_checkpoint_pack", _INT, [_T] * 3 + [_P]),
+    ("dcn1d_checkpoint_unpack", _INT, [_T] * 5 + [_P]),
+    ("dcn1d_backward_checkpoint_workspace_size", _I64,
+     [_T] * 8 + [_I64] * 6 + [_INT] + [_T] * 5),
+    ("dcn1d_backward_checkpoint", _INT,
+     [_T] * 8 + [_I64] * 6 + [_INT] + [_T] * 5 + [_P, ctypes.c_size_t, _P]),
 ]
 
 
@@ -608,3 +621,192 @@ def dcn1d_packed_forward(x, dw_weight, dw_bias, off_weight, off_bias, mask_weigh
     if not with_offsets:
         return out
     return (out, (off_t, mask_t)) if mask_weight is not None else (out, off_t)
+
+
+# ------------------------------------------------- layer norm and 8-bit checkpoints
+
+
+class Checkpoint8(NamedTuple):
+    """An activation [B, C, L] kept in 8 bits until the backward pass (include/dcn1d.h,
+    dcn1d_checkpoint_pack): int8 ``codes`` [B, C, L] and one uint8 ``scales`` entry for each
+    block of 32 values of a row."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+CHECKPOINT_BLOCK = 32
+
+
+def _scales_shape(B, C, L):
+    blocks = -(-(C if L == 1 else L) // CHECKPOINT_BLOCK)
+    return (B, blocks, 1) if L == 1 else (B, C, blocks)
+
+
+def _empty_checkpoint(shape, dev):
+    if len(shape) != 3:
+        raise ValueError("a checkpoint is of a [B, C, L] tensor")
+    return Checkpoint8(torch.empty(shape, dtype=torch.int8, device=dev),
+                       torch.empty(_scales_shape(*shape), dtype=torch.uint8, device=dev))
+
+
+def _on(dev, stream):
+    """Context in which a call's tensors are allocated and its work is enqueued: the given
+    stream (memory allocated here then belongs to it), else the device's current one."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() == dev.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _check_status(st, where):
+    if st != 0:
+        raise Dcn1dError(st, where)
+
+
+def _workspace(need, workspace, dev, where):
+    """(pointer, bytes, tensor) of a call's scratch of ``need`` bytes."""
+    if need < 0:
+        raise Dcn1dError(-need, where + "_workspace_size")
+    if need == 0:
+        return None, 0, None
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace.device != dev or workspace.dtype != torch.uint8 or workspace.numel() < need:
+        raise ValueError(f"workspace must be a uint8 tensor of >= {need} bytes on {dev}")
+    return workspace.data_ptr(), workspace.numel(), workspace
+
+
+def dcn1d_layer_norm_forward(x, gamma=None, beta=None, eps=1e-5, stats=True, checkpoint=None,
+                             out=None, stream=None):
+    """Layer norm over the channels of x [B, C, L]; returns (y, mean, rstd, checkpoint).
+
+    ``gamma`` and ``beta`` [C] in x's dtype, or None.  mean and rstd are float32 [B, L]
+    (None with ``stats=False``).  ``checkpoint=True`` (or a Checkpoint8 to write into) also
+    keeps the normalised values (x - mean) * rstd in 8 bits for dcn1d_layer_norm_backward
+    and dcn1d_backward_checkpoint; None otherwise.  ``out`` receives y when given.  Runs on
+    ``stream`` (default: the current torch stream of x's device); does not synchronise.
+    """
+    given = checkpoint if isinstance(checkpoint, tuple) else (None, None)
+    dev = _check_device((x, gamma, beta, out, *given))
+    lib = load()
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty_like(x)
+        mean = rstd = None
+        if stats:
+            B, _, L = x.shape
+            mean, rstd = torch.empty((2, B, L), dtype=torch.float32, device=dev)
+        kept = Checkpoint8(*given) if given[0] is not None else None
+        if kept is None and checkpoint:
+            kept = _empty_checkpoint(x.shape, dev)
+        refs = [_ref(_desc(t)) for t in (x, gamma, beta, out, mean, rstd, *(kept or given))]
+        st = lib.dcn1d_layer_norm_forward(*refs[:3], eps, *refs[3:], _P(_stream_ptr(stream, dev)))
+    _check_status(st, "dcn1d_layer_norm_forward")
+    return out, mean, rstd, kept
+
+
+NORM_GRADS = ("x", "gamma", "beta")
+
+
+def dcn1d_layer_norm_backward(x, gamma, mean, rstd, grad_y, wanted=NORM_GRADS, grads=None,
+                              workspace=None, stream=None):
+    """Gradients of sum(grad_y * y) of dcn1d_layer_norm_forward.
+
+    ``x`` is the forward's input (with its ``mean`` and ``rstd``), or the Checkpoint8 that
+    the forward kept (``mean`` is then None).  Returns a dict {name: tensor} for the names in
+    ``wanted`` (a subset of "x", "gamma", "beta") in grad_y's dtype.  ``grads`` may supply
+    some of those tensors (they are overwritten); the rest, and the scratch the call needs,
+    are allocated with torch unless a uint8 CUDA tensor ``workspace`` is given.  Runs on
+    ``stream``; does not synchronise.
+    """
+    unknown = set(wanted) - set(NORM_GRADS)
+    if unknown:
+        raise ValueError(f"unknown gradients {sorted(unknown)}")
+    codes, scales = x if isinstance(x, tuple) else (None, None)
+    x = None if codes is not None else x
+    res = {n: (grads or {}).get(n) for n in wanted}
+    dev = _check_device((grad_y, x, gamma, mean, rstd, codes, scales, *res.values()))
+    lib = load()
+    with _on(dev, stream):
+        for n in wanted:
+            if res[n] is None:
+                res[n] = torch.empty(grad_y.shape if n == "x" else grad_y.shape[1:2],
+                                     dtype=grad_y.dtype, device=dev)
+        refs = [_ref(_desc(t)) for t in (x, gamma, mean, rstd, codes, scales, grad_y,
+                                         *(res.get(n) for n in NORM_GRADS))]
+        need = int(lib.dcn1d_layer_norm_backward_workspace_size(*refs))
+        ptr, size, workspace = _workspace(need, workspace, dev, "dcn1d_layer_norm_backward")
+        st = lib.dcn1d_layer_norm_backward(*refs, _P(ptr), size, _P(_stream_ptr(stream, dev)))
+    _check_status(st, "dcn1d_layer_norm_backward")
+    return res
+
+
+def dcn1d_checkpoint_pack(x, out=None, stream=None):
+    """x [B, C, L] in 8 bits a value: a Checkpoint8 (``out`` when given).  Does not
+    synchronise."""
+    dev = _check_device((x, *(out or ())))
+    lib = load()
+    with _on(dev, stream):
+        kept = Checkpoint8(*out) if out is not None else _empty_checkpoint(x.shape, dev)
+        refs = [_ref(_desc(t)) for t in (x, *kept)]
+        st = lib.dcn1d_checkpoint_pack(*refs, _P(_stream_ptr(stream, dev)))
+    _check_status(st, "dcn1d_checkpoint_pack")
+    return kept
+
+
+def dcn1d_checkpoint_unpack(checkpoint, gamma=None, beta=None, dtype=torch.float32, out=None,
+                            stream=None):
+    """The values of a Checkpoint8 as a [B, C, L] tensor of ``dtype`` (of ``out`` when given):
+    gamma * value + beta with ``gamma`` and ``beta`` [C] of that dtype, else the values
+    themselves.  Does not synchronise."""
+    codes, scales = checkpoint
+    dev = _check_device((codes, scales, gamma, beta, out))
+    lib = load()
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(codes.shape, dtype=dtype, device=dev)
+        refs = [_ref(_desc(t)) for t in (codes, scales, gamma, beta, out)]
+        st = lib.dcn1d_checkpoint_unpack(*refs, _P(_stream_ptr(stream, dev)))
+    _check_status(st, "dcn1d_checkpoint_unpack")
+    return out
+
+
+def dcn1d_backward_checkpoint(checkpoint, offsets, mask, weight, grad_out, stride=1, padding=0,
+                              dilation=1, groups=1, offset_groups=1, unconstrained=False,
+                              gamma=None, beta=None, wanted=GRADS, grads=None, workspace=None,
+                              stream=None):
+    """dcn1d_backward with the layer's input given as a Checkpoint8.
+
+    The input is dcn1d_checkpoint_unpack(checkpoint, gamma, beta) in grad_out's dtype: pass
+    the norm's ``gamma`` and ``beta`` with the checkpoint that dcn1d_layer_norm_forward kept,
+    or neither with a checkpoint of the input itself.  The other arguments and the result
+    are dcn1d_backward's.
+    """
+    wanted = tuple(n for n in wanted if n != "mask" or mask is not None)
+    unknown = set(wanted) - set(GRADS)
+    if unknown:
+        raise ValueError(f"unknown gradients {sorted(unknown)}")
+    codes, scales = checkpoint
+    res = {n: (grads or {}).get(n) for n in wanted}
+    dev = _check_device((grad_out, codes, scales, gamma, beta, offsets, mask, weight,
+                         *res.values()))
+    lib = load()
+    pl, pr = resolve_padding(padding, weight.shape[2], stride, dilation)
+    args = (stride, pl, pr, dilation, groups, offset_groups, int(bool(unconstrained)))
+    with _on(dev, stream):
+        shapes = {"x": codes.shape, "offsets": offsets.shape, "weight": weight.shape,
+                  "mask": offsets.shape, "bias": weight.shape[:1]}
+        for n in wanted:
+            if res[n] is None:
+                res[n] = torch.empty(shapes[n], dtype=grad_out.dtype, device=dev)
+        refs = [_ref(_desc(t)) for t in (codes, scales, gamma, beta, offsets, mask, weight,
+                                         grad_out, *(res.get(n) for n in GRADS))]
+        need = int(lib.dcn1d_backward_checkpoint_workspace_size(*refs[:8], *args, *refs[8:]))
+        ptr, size, workspace = _workspace(need, workspace, dev, "dcn1d_backward_checkpoint")
+        st = lib.dcn1d_backward_checkpoint(*refs[:8], *args, *refs[8:], _P(ptr), size,
+                                           _P(_stream_ptr(stream, dev)))
+    _check_status(st, "dcn1d_backward_checkpoint")
+    return res

@@ -1,10 +1,12 @@
 // The C ABI (include/dcn1d.h): argument validation, kernel selection and
 // launch on the caller's stream.  Allocates nothing and never synchronises.
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
 #include <mutex>
 
+#include "checkpoint.cuh"
 #include "sm100.cuh"
 
 namespace dcn1d {
@@ -382,6 +384,127 @@ int packed_prepare(const dcn1d_tensor *x, const dcn1d_tensor *dw_w, const dcn1d_
         return DCN1D_OK;
     }
     lay->total = lay->fwd_offset + round256(workspace_bytes(*P));
+    return DCN1D_OK;
+}
+
+// check_desc for one given dtype, with the given shape.
+int check_typed(const dcn1d_tensor *t, int dtype, int ndim, int64_t a, int64_t b = -1,
+                int64_t c = -1) {
+    if (!t)
+        return DCN1D_ERR_NULL;
+    if (t->dtype != dtype)
+        return DCN1D_ERR_DTYPE;
+    if (t->ndim != ndim)
+        return DCN1D_ERR_SHAPE;
+    const int64_t want[3] = {a, b, c};
+    for (int i = 0; i < ndim; ++i)
+        if (t->shape[i] != want[i])
+            return DCN1D_ERR_SHAPE;
+    if (!t->data && numel(t) > 0)
+        return DCN1D_ERR_NULL;
+    return DCN1D_OK;
+}
+
+// The sizes of an activation [B, C, L] of the norm or of a checkpoint.
+int check_sizes(int64_t B, int64_t C, int64_t L) {
+    if (B < 0 || C < 1 || L < 0)
+        return DCN1D_ERR_SHAPE;
+    const int64_t lim = (int64_t)1 << 31;
+    if (B >= lim || C >= lim || L >= lim || (L > 0 && B >= lim / L))
+        return DCN1D_ERR_UNSUPPORTED;
+    // element counts stay far inside int64: B * L < 2^31 and C < 2^31
+    return norm_grid_ok(B, L) ? DCN1D_OK : DCN1D_ERR_UNSUPPORTED;
+}
+
+// Codes and scales of a checkpoint of [B, C, L].
+int check_checkpoint(const dcn1d_tensor *codes, const dcn1d_tensor *scales, int64_t B, int64_t C,
+                     int64_t L) {
+    const int st = check_typed(codes, DCN1D_I8, 3, B, C, L);
+    if (st != DCN1D_OK)
+        return st;
+    if (L == 1)
+        return check_typed(scales, DCN1D_U8, 3, B, ck_blocks(C), 1);
+    return check_typed(scales, DCN1D_U8, 3, B, C, ck_blocks(L));
+}
+
+template <class T> T *data_of(const dcn1d_tensor *t) {
+    return t ? static_cast<T *>(t->data) : nullptr;
+}
+
+int validate_norm_grad(const dcn1d_tensor *x, const dcn1d_tensor *gamma, const dcn1d_tensor *mean,
+                       const dcn1d_tensor *rstd, const dcn1d_tensor *codes,
+                       const dcn1d_tensor *scales, const dcn1d_tensor *gy, const dcn1d_tensor *gx,
+                       const dcn1d_tensor *ggamma, const dcn1d_tensor *gbeta, NormGrad *P) {
+    int st;
+    if ((st = check_desc(gy, 3)))
+        return st;
+    const int dt = gy->dtype;
+    const int64_t B = gy->shape[0], C = gy->shape[1], L = gy->shape[2];
+    if ((st = check_sizes(B, C, L)))
+        return st;
+    if ((codes || scales) && (x || mean))
+        return DCN1D_ERR_ARG;   // the values come from one of the two
+    if (codes || scales) {
+        if ((st = check_checkpoint(codes, scales, B, C, L)))
+            return st;
+    } else if ((st = check_typed(x, dt, 3, B, C, L)) ||
+               (st = check_typed(mean, DCN1D_F32, 2, B, L))) {
+        return st;
+    }
+    if ((st = check_typed(rstd, DCN1D_F32, 2, B, L)))
+        return st;
+    for (const dcn1d_tensor *t : {gamma, ggamma, gbeta})
+        if (t && (st = check_typed(t, dt, 1, C)))
+            return st;
+    if (gx && (st = check_typed(gx, dt, 3, B, C, L)))
+        return st;
+    *P = NormGrad{B, C, L, dt, data_of<void>(x), data_of<void>(gamma), gy->data,
+                  data_of<float>(mean), data_of<float>(rstd), data_of<int8_t>(codes),
+                  data_of<uint8_t>(scales), data_of<void>(gx), data_of<void>(ggamma),
+                  data_of<void>(gbeta)};
+    P->from_codes = codes != nullptr;
+    return DCN1D_OK;
+}
+
+// A backward whose x is a checkpoint: the checkpoint's own checks, then the backward's with
+// x as a tensor of grad_out's dtype at the start of the workspace.
+struct CheckpointBackward {
+    CkProblem ck;
+    Problem P;
+    BackwardGrads G;
+    size_t x_bytes, total;
+};
+
+int validate_checkpoint_backward(
+    const dcn1d_tensor *codes, const dcn1d_tensor *scales, const dcn1d_tensor *gamma,
+    const dcn1d_tensor *beta, const dcn1d_tensor *off, const dcn1d_tensor *mask,
+    const dcn1d_tensor *w, const dcn1d_tensor *gout, int64_t stride, int64_t padding,
+    int64_t padding_right, int64_t dilation, int64_t groups, int64_t offset_groups,
+    int unconstrained, const dcn1d_tensor *gx, const dcn1d_tensor *goff,
+    const dcn1d_tensor *gmask, const dcn1d_tensor *gw, const dcn1d_tensor *gbias,
+    CheckpointBackward *R) {
+    int st;
+    if (!codes || !scales || !gout)
+        return DCN1D_ERR_NULL;
+    if (codes->ndim != 3)
+        return DCN1D_ERR_SHAPE;
+    const int64_t B = codes->shape[0], C = codes->shape[1], L = codes->shape[2];
+    if ((st = check_sizes(B, C, L)) || (st = check_checkpoint(codes, scales, B, C, L)))
+        return st;
+    dcn1d_tensor x = *codes;
+    x.dtype = gout->dtype;
+    x.data = reinterpret_cast<void *>((uintptr_t)256);   // the workspace's start, set at launch
+    if ((st = validate_backward(&x, off, mask, w, gout, stride, padding, padding_right, dilation,
+                                groups, offset_groups, unconstrained, gx, goff, gmask, gw, gbias,
+                                &R->P, &R->G)))
+        return st;
+    for (const dcn1d_tensor *t : {gamma, beta})
+        if (t && (st = check_typed(t, x.dtype, 1, C)))
+            return st;
+    R->ck = CkProblem{B, C, L, x.dtype, nullptr, data_of<void>(gamma), data_of<void>(beta),
+                      codes->data, scales->data, nullptr};
+    R->x_bytes = round256((size_t)(B * C * L) * (x.dtype == DCN1D_F32 ? 4 : 2));
+    R->total = R->x_bytes + backward_workspace(R->P, R->G);
     return DCN1D_OK;
 }
 
@@ -852,6 +975,172 @@ int dcn1d_packed_forward(const dcn1d_tensor *x, const dcn1d_tensor *dw_weight,
         cudaSuccess)
         return DCN1D_ERR_LAUNCH;
     g_last_launches = 1 + launches;
+    return DCN1D_OK;
+}
+
+int dcn1d_layer_norm_forward(const dcn1d_tensor *x, const dcn1d_tensor *gamma,
+                             const dcn1d_tensor *beta, float eps, dcn1d_tensor *y,
+                             dcn1d_tensor *mean, dcn1d_tensor *rstd, dcn1d_tensor *codes,
+                             dcn1d_tensor *scales, void *stream) {
+    g_last_launches = 0;
+    int st;
+    if (!x || !y)
+        return DCN1D_ERR_NULL;
+    if ((st = check_desc(x, 3)))
+        return st;
+    const int dt = x->dtype;
+    const int64_t B = x->shape[0], C = x->shape[1], L = x->shape[2];
+    if ((st = check_sizes(B, C, L)))
+        return st;
+    if (!(eps >= 0.0f) || isinf(eps))
+        return DCN1D_ERR_ARG;
+    if ((st = check_typed(y, dt, 3, B, C, L)))
+        return st;
+    for (const dcn1d_tensor *t : {gamma, beta})
+        if (t && (st = check_typed(t, dt, 1, C)))
+            return st;
+    for (const dcn1d_tensor *t : {mean, rstd})
+        if (t && (st = check_typed(t, DCN1D_F32, 2, B, L)))
+            return st;
+    if ((codes || scales) && (st = check_checkpoint(codes, scales, B, C, L)))
+        return st;
+    if (B == 0 || L == 0)
+        return DCN1D_OK;
+    const NormProblem P{B, C, L, dt, eps, x->data, data_of<void>(gamma), data_of<void>(beta),
+                        y->data, data_of<float>(mean), data_of<float>(rstd),
+                        data_of<int8_t>(codes), data_of<uint8_t>(scales)};
+    if (launch_norm(P, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return DCN1D_ERR_LAUNCH;
+    g_last_launches = 1;
+    return DCN1D_OK;
+}
+
+int64_t dcn1d_layer_norm_backward_workspace_size(
+    const dcn1d_tensor *x, const dcn1d_tensor *gamma, const dcn1d_tensor *mean,
+    const dcn1d_tensor *rstd, const dcn1d_tensor *codes, const dcn1d_tensor *scales,
+    const dcn1d_tensor *grad_y, const dcn1d_tensor *grad_x, const dcn1d_tensor *grad_gamma,
+    const dcn1d_tensor *grad_beta) {
+    NormGrad P;
+    const int st = validate_norm_grad(x, gamma, mean, rstd, codes, scales, grad_y, grad_x,
+                                      grad_gamma, grad_beta, &P);
+    return st != DCN1D_OK ? -(int64_t)st : (int64_t)norm_grad_workspace(P);
+}
+
+int dcn1d_layer_norm_backward(const dcn1d_tensor *x, const dcn1d_tensor *gamma,
+                              const dcn1d_tensor *mean, const dcn1d_tensor *rstd,
+                              const dcn1d_tensor *codes, const dcn1d_tensor *scales,
+                              const dcn1d_tensor *grad_y, dcn1d_tensor *grad_x,
+                              dcn1d_tensor *grad_gamma, dcn1d_tensor *grad_beta, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+    g_last_launches = 0;
+    NormGrad P;
+    const int st = validate_norm_grad(x, gamma, mean, rstd, codes, scales, grad_y, grad_x,
+                                      grad_gamma, grad_beta, &P);
+    if (st != DCN1D_OK)
+        return st;
+    const size_t need = norm_grad_workspace(P);
+    if (need > 0 && !workspace)
+        return DCN1D_ERR_NULL;
+    if (need > workspace_bytes || (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return DCN1D_ERR_ARG;
+    int launches = 0;
+    if (launch_norm_grad(P, workspace, static_cast<cudaStream_t>(stream), &launches) !=
+        cudaSuccess)
+        return DCN1D_ERR_LAUNCH;
+    g_last_launches = launches;
+    return DCN1D_OK;
+}
+
+int dcn1d_checkpoint_pack(const dcn1d_tensor *x, dcn1d_tensor *codes, dcn1d_tensor *scales,
+                          void *stream) {
+    g_last_launches = 0;
+    int st;
+    if ((st = check_desc(x, 3)))
+        return st;
+    const int64_t B = x->shape[0], C = x->shape[1], L = x->shape[2];
+    if ((st = check_sizes(B, C, L)) || (st = check_checkpoint(codes, scales, B, C, L)))
+        return st;
+    if (B == 0 || L == 0)
+        return DCN1D_OK;
+    const CkProblem P{B, C, L, x->dtype, x->data, nullptr, nullptr, codes->data, scales->data,
+                      nullptr};
+    if (launch_checkpoint_pack(P, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return DCN1D_ERR_LAUNCH;
+    g_last_launches = 1;
+    return DCN1D_OK;
+}
+
+int dcn1d_checkpoint_unpack(const dcn1d_tensor *codes, const dcn1d_tensor *scales,
+                            const dcn1d_tensor *gamma, const dcn1d_tensor *beta,
+                            dcn1d_tensor *out, void *stream) {
+    g_last_launches = 0;
+    int st;
+    if ((st = check_desc(out, 3)))
+        return st;
+    const int64_t B = out->shape[0], C = out->shape[1], L = out->shape[2];
+    if ((st = check_sizes(B, C, L)) || (st = check_checkpoint(codes, scales, B, C, L)))
+        return st;
+    for (const dcn1d_tensor *t : {gamma, beta})
+        if (t && (st = check_typed(t, out->dtype, 1, C)))
+            return st;
+    if (B == 0 || L == 0)
+        return DCN1D_OK;
+    const CkProblem P{B, C, L, out->dtype, nullptr, data_of<void>(gamma), data_of<void>(beta),
+                      codes->data, scales->data, out->data};
+    if (launch_checkpoint_unpack(P, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return DCN1D_ERR_LAUNCH;
+    g_last_launches = 1;
+    return DCN1D_OK;
+}
+
+int64_t dcn1d_backward_checkpoint_workspace_size(
+    const dcn1d_tensor *codes, const dcn1d_tensor *scales, const dcn1d_tensor *gamma,
+    const dcn1d_tensor *beta, const dcn1d_tensor *offsets, const dcn1d_tensor *mask,
+    const dcn1d_tensor *weight, const dcn1d_tensor *grad_out, int64_t stride,
+    int64_t padding_left, int64_t padding_right, int64_t dilation, int64_t groups,
+    int64_t offset_groups, int unconstrained, const dcn1d_tensor *grad_x,
+    const dcn1d_tensor *grad_offsets, const dcn1d_tensor *grad_mask,
+    const dcn1d_tensor *grad_weight, const dcn1d_tensor *grad_bias) {
+    CheckpointBackward R;
+    const int st = validate_checkpoint_backward(
+        codes, scales, gamma, beta, offsets, mask, weight, grad_out, stride, padding_left,
+        padding_right, dilation, groups, offset_groups, unconstrained, grad_x, grad_offsets,
+        grad_mask, grad_weight, grad_bias, &R);
+    return st != DCN1D_OK ? -(int64_t)st : (int64_t)R.total;
+}
+
+int dcn1d_backward_checkpoint(
+    const dcn1d_tensor *codes, const dcn1d_tensor *scales, const dcn1d_tensor *gamma,
+    const dcn1d_tensor *beta, const dcn1d_tensor *offsets, const dcn1d_tensor *mask,
+    const dcn1d_tensor *weight, const dcn1d_tensor *grad_out, int64_t stride,
+    int64_t padding_left, int64_t padding_right, int64_t dilation, int64_t groups,
+    int64_t offset_groups, int unconstrained, dcn1d_tensor *grad_x, dcn1d_tensor *grad_offsets,
+    dcn1d_tensor *grad_mask, dcn1d_tensor *grad_weight, dcn1d_tensor *grad_bias,
+    void *workspace, size_t workspace_bytes, void *stream) {
+    g_last_launches = 0;
+    CheckpointBackward R;
+    const int st = validate_checkpoint_backward(
+        codes, scales, gamma, beta, offsets, mask, weight, grad_out, stride, padding_left,
+        padding_right, dilation, groups, offset_groups, unconstrained, grad_x, grad_offsets,
+        grad_mask, grad_weight, grad_bias, &R);
+    if (st != DCN1D_OK)
+        return st;
+    if (R.total > 0 && !workspace)
+        return DCN1D_ERR_NULL;
+    if (R.total > workspace_bytes || (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return DCN1D_ERR_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int launches = 0, unpacked = 0;
+    if (R.ck.B > 0) {
+        R.P.x = R.ck.out = workspace;
+        if (launch_checkpoint_unpack(R.ck, s) != cudaSuccess)
+            return DCN1D_ERR_LAUNCH;
+        unpacked = 1;
+    }
+    if (launch_backward(R.P, R.G, static_cast<char *>(workspace) + R.x_bytes, s, &launches) !=
+        cudaSuccess)
+        return DCN1D_ERR_LAUNCH;
+    g_last_launches = unpacked + launches;
     return DCN1D_OK;
 }
 

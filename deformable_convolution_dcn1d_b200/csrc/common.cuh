@@ -127,6 +127,47 @@ bool packed_fused_supported(const TrunkProblem &T, const Problem &P);
 cudaError_t launch_packed_fused(const TrunkProblem &T, const Problem &P, cudaStream_t stream);
 // Launches the trunk; *kernel receives the name of the kernel chosen.
 cudaError_t launch_trunk(const TrunkProblem &T, cudaStream_t stream, const char **kernel);
+// Layer norm over C of [B, C, L] (norm.cu).  mean and rstd are fp32 [B, L]; codes and scales
+// are the checkpoint of the normalised values (checkpoint.cuh).  Every pointer but x, y,
+// gy and rstd may be NULL; the backward reads codes and scales, or x and mean.
+struct NormProblem {
+    int64_t B, C, L;
+    int dtype;
+    float eps;
+    const void *x, *gamma, *beta;
+    void *y;
+    float *mean, *rstd;
+    int8_t *codes;
+    uint8_t *scales;
+};
+struct NormGrad {
+    int64_t B, C, L;
+    int dtype;
+    const void *x, *gamma, *gy;
+    const float *mean, *rstd;
+    const int8_t *codes;
+    const uint8_t *scales;
+    void *gx, *ggamma, *gbeta;
+    bool from_codes;
+};
+bool norm_grid_ok(int64_t B, int64_t L);
+cudaError_t launch_norm(const NormProblem &P, cudaStream_t stream);
+size_t norm_grad_workspace(const NormGrad &P);
+cudaError_t launch_norm_grad(const NormGrad &P, void *workspace, cudaStream_t stream,
+                             int *launches);
+// The 8-bit checkpoint (checkpoint.cu): packing `in`, or reading one back into `out` (of
+// `dtype`), through gamma and beta where given.
+struct CkProblem {
+    int64_t B, C, L;
+    int dtype;
+    const void *in, *gamma, *beta;
+    void *codes, *scales, *out;
+    bool along_c() const { return L == 1; }   // blocks run along the channels
+};
+cudaError_t launch_checkpoint_pack(const CkProblem &P, cudaStream_t stream);
+cudaError_t launch_checkpoint_unpack(const CkProblem &P, cudaStream_t stream);
+// SM count of the current device, or `other` where it cannot be read (no device).
+int sm_count_or(int other);
 cudaError_t launch_sample_index(const void *off, int dtype, int B, int G, int L_out, int K,
                                 int L_in, int stride, int padding, int dilation,
                                 int unconstrained, int32_t *i0, float *frac,

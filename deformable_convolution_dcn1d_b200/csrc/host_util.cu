@@ -52,6 +52,11 @@ int sm_count() {
     return counts[dev].load(std::memory_order_relaxed);
 }
 
+int sm_count_or(int other) {
+    const int n = sm_count();
+    return n > 0 ? n : other;
+}
+
 cudaError_t ensure_smem(const void *kernel, int bytes) {
     struct Entry {
         const void *fn;

@@ -63,7 +63,9 @@ typedef enum dcn1d_status {
 typedef enum dcn1d_dtype {
     DCN1D_F32 = 0,             /* IEEE float32                                             */
     DCN1D_BF16 = 1,            /* bfloat16                                                 */
-    DCN1D_F16 = 2              /* IEEE float16 (binary16)                                  */
+    DCN1D_F16 = 2,             /* IEEE float16 (binary16)                                  */
+    DCN1D_I8 = 3,              /* int8: the codes of an 8-bit checkpoint only              */
+    DCN1D_U8 = 4               /* uint8: the step bytes of an 8-bit checkpoint only        */
 } dcn1d_dtype;
 
 /* A dense, contiguous, row-major device array of `ndim` (<= 4) dimensions. */
@@ -408,6 +410,120 @@ const char *dcn1d_packed_forward_kernel_name(
     const dcn1d_tensor *bias, int64_t stride, int64_t padding_left, int64_t padding_right,
     int64_t dilation, int64_t groups, int64_t offset_groups, int unconstrained,
     const dcn1d_tensor *offsets_out, const dcn1d_tensor *mask_out, const dcn1d_tensor *out);
+
+/*
+ * Layer norm over the channels of x [B, C, L]: for every (b, l)
+ *
+ *   mean = sum_c x / C,   rstd = 1 / sqrt(sum_c (x - mean)^2 / C + eps)
+ *   v = (x - mean) * rstd,   y[b,c,l] = gamma[c] * v + beta[c]
+ *
+ *   x            [B, C, L]                             required; C >= 1, B or L may be 0
+ *   gamma, beta  [C] in x's dtype, each or NULL        (1 and 0)
+ *   eps          finite, >= 0
+ *   y            [B, C, L] in x's dtype                required, written entirely
+ *   mean, rstd   [B, L] F32, each or NULL              what the backward pass reads
+ *   codes, scales  the 8-bit checkpoint of v (see dcn1d_checkpoint_pack), both or NULL
+ *
+ * L == 1 normalises rows of C contiguous values (single tokens).  Arithmetic and
+ * statistics are fp32 (the variance is taken about the mean, in a second pass over values
+ * held on chip or read again); y is rounded once.  A position that holds a NaN or an
+ * infinity gives NaN at that position only; in the checkpoint it marks its blocks.  One
+ * launch, no scratch memory.  Sizes: B * L < 2^31 and C < 2^31; the number of elements
+ * may pass 2^31.
+ */
+int dcn1d_layer_norm_forward(const dcn1d_tensor *x, const dcn1d_tensor *gamma,
+                             const dcn1d_tensor *beta, float eps, dcn1d_tensor *y,
+                             dcn1d_tensor *mean, dcn1d_tensor *rstd, dcn1d_tensor *codes,
+                             dcn1d_tensor *scales, void *stream);
+
+/*
+ * The gradients of sum(grad_y * y): with d = gamma[c] * grad_y,
+ *
+ *   grad_x        = rstd * (d - sum_c d / C - v * sum_c (d * v) / C)
+ *   grad_gamma[c] = sum_{b,l} grad_y * v,   grad_beta[c] = sum_{b,l} grad_y
+ *
+ * v comes from x and mean, or from the checkpoint that the forward wrote (x and mean are
+ * then NULL): pass x and mean, or codes and scales, not both (DCN1D_ERR_ARG).  rstd and
+ * grad_y are required; gamma is the forward's (NULL: 1).  grad_x [B, C, L], grad_gamma and
+ * grad_beta [C] are in grad_y's dtype, each NULL when not wanted, and overwritten.  Sums
+ * are fp32 in a fixed order: equal calls on one device give equal bits.
+ *
+ * Scratch: `workspace` (256-byte aligned) of dcn1d_layer_norm_backward_workspace_size()
+ * bytes, used only by the work enqueued on `stream`; 0 when neither grad_gamma nor
+ * grad_beta is wanted.  Too small or misaligned: DCN1D_ERR_ARG; NULL with a non-zero
+ * need: DCN1D_ERR_NULL.  The size query is host only; a negative value is minus the status
+ * code of invalid arguments.  It depends on the current device's SM count.
+ */
+int64_t dcn1d_layer_norm_backward_workspace_size(
+    const dcn1d_tensor *x, const dcn1d_tensor *gamma, const dcn1d_tensor *mean,
+    const dcn1d_tensor *rstd, const dcn1d_tensor *codes, const dcn1d_tensor *scales,
+    const dcn1d_tensor *grad_y, const dcn1d_tensor *grad_x, const dcn1d_tensor *grad_gamma,
+    const dcn1d_tensor *grad_beta);
+
+int dcn1d_layer_norm_backward(const dcn1d_tensor *x, const dcn1d_tensor *gamma,
+                              const dcn1d_tensor *mean, const dcn1d_tensor *rstd,
+                              const dcn1d_tensor *codes, const dcn1d_tensor *scales,
+                              const dcn1d_tensor *grad_y, dcn1d_tensor *grad_x,
+                              dcn1d_tensor *grad_gamma, dcn1d_tensor *grad_beta, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * The 8-bit checkpoint of an activation: what a training step keeps between the forward
+ * and the backward pass instead of the tensor, 1 + 1/32 bytes a value.
+ *
+ * A row of x [B, C, L] is the L positions of one (b, c); when L == 1 it is the C channels
+ * of one b.  A row is cut into blocks of 32 values (the last may be shorter).
+ *
+ *   codes   [B, C, L] I8                      value = code * 2^(s - 127), code in [-127, 127]
+ *   scales  [B, C, ceil(L / 32)] U8           the block's s: the biased exponent of its step
+ *           ([B, ceil(C / 32), 1] when L == 1)
+ *
+ * The step is the smallest power of two, at least 2^-126, at which the block's largest
+ * magnitude rounds to a code of at most 127; a code is the nearest integer to value / step
+ * (ties to even).  A value is off by at most half a step, so by at most 2^-7 of its block's
+ * largest magnitude (for magnitudes from 2^-119).  A block whose largest magnitude is
+ * within 0.4 % of x's dtype's largest finite number saturates at code 127.  A block that
+ * holds a NaN or an infinity gets s = 255 and reads back as NaN throughout.
+ * Packing what was unpacked to F32 or BF16 gives the same values back.
+ */
+int dcn1d_checkpoint_pack(const dcn1d_tensor *x, dcn1d_tensor *codes, dcn1d_tensor *scales,
+                          void *stream);
+
+/*
+ * out = gamma[c] * value + beta[c] (gamma, beta [C] in out's dtype, each or NULL: 1 and 0),
+ * the product and the sum rounded to fp32 and the result to out's dtype (F32, BF16, F16):
+ * a checkpoint's values, or from the checkpoint that dcn1d_layer_norm_forward wrote the
+ * norm's output.  Values past F16's range become infinities there.
+ */
+int dcn1d_checkpoint_unpack(const dcn1d_tensor *codes, const dcn1d_tensor *scales,
+                            const dcn1d_tensor *gamma, const dcn1d_tensor *beta,
+                            dcn1d_tensor *out, void *stream);
+
+/*
+ * dcn1d_backward_lr with the layer's input x given as an 8-bit checkpoint: x is what
+ * dcn1d_checkpoint_unpack gives for codes, scales, gamma and beta (the last two NULL for a
+ * checkpoint of x itself; the norm's weights when x was the norm's output) in grad_out's
+ * dtype.  grad_x is the gradient with respect to that x.  All other arguments, errors and
+ * remarks as for dcn1d_backward_lr; the workspace (256-byte aligned) has the size that
+ * dcn1d_backward_checkpoint_workspace_size gives.
+ */
+int64_t dcn1d_backward_checkpoint_workspace_size(
+    const dcn1d_tensor *codes, const dcn1d_tensor *scales, const dcn1d_tensor *gamma,
+    const dcn1d_tensor *beta, const dcn1d_tensor *offsets, const dcn1d_tensor *mask,
+    const dcn1d_tensor *weight, const dcn1d_tensor *grad_out, int64_t stride,
+    int64_t padding_left, int64_t padding_right, int64_t dilation, int64_t groups,
+    int64_t offset_groups, int unconstrained, const dcn1d_tensor *grad_x,
+    const dcn1d_tensor *grad_offsets, const dcn1d_tensor *grad_mask,
+    const dcn1d_tensor *grad_weight, const dcn1d_tensor *grad_bias);
+
+int dcn1d_backward_checkpoint(
+    const dcn1d_tensor *codes, const dcn1d_tensor *scales, const dcn1d_tensor *gamma,
+    const dcn1d_tensor *beta, const dcn1d_tensor *offsets, const dcn1d_tensor *mask,
+    const dcn1d_tensor *weight, const dcn1d_tensor *grad_out, int64_t stride,
+    int64_t padding_left, int64_t padding_right, int64_t dilation, int64_t groups,
+    int64_t offset_groups, int unconstrained, dcn1d_tensor *grad_x, dcn1d_tensor *grad_offsets,
+    dcn1d_tensor *grad_mask, dcn1d_tensor *grad_weight, dcn1d_tensor *grad_bias,
+    void *workspace, size_t workspace_bytes, void *stream);
 
 /* A static, human-readable name of a status code ("DCN1D_OK", ...). Never NULL. */
 const char *dcn1d_status_string(int status);
