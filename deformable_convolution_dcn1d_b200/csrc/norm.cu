@@ -6,17 +6,768 @@
 //   grad_x = rstd (d - A - v S)
 //   grad_gamma[c] = sum_{b,l} grad_y v,   grad_beta[c] = sum_{b,l} grad_y
 //
-// The normalised axis is strided by L in memory.  A block takes TL consecutive positions of
-// one b (TL a power of two up to 32, at least L where L is shorter); its lanes run along
-// them, so a warp covers 32 / TL channels, eight warps eight times that, and the block
-// walks all C channels.  With L == 1 the lanes run along the channels.
+// A few flops a value: the bytes bound all of it.  The normalised axis is strided by L in
+// memory, so the tile kernels keep a tile of TW positions x all channels on chip and read
+// every value once: TW * sizeof(T) = 128 bytes of each channel's row (less when L is
+// shorter), a whole DRAM burst, in shared memory.  Eight lanes hold a row, a 16-byte chunk
+// each, so a thread owns V = 16 / sizeof(T) positions and every eighth warp's rows; sums
+// over channels stay in registers until one exchange between lanes, warps and, where the
+// channels are split over the blocks of a cluster, distributed shared memory.  Each warp
+// takes its sums about its own rounded mean k, s1 = sum (x - k) and s2 = sum (x - k)^2, and
+// groups of n_i values are joined about a common k by
+//   s1 = sum_i s1_i + n_i d_i,  s2 = sum_i s2_i + 2 d_i s1_i + n_i d_i^2,  d_i = k_i - k:
+// one exchange instead of one for the mean and one for the variance, and no difference of
+// large squares however far the mean is from zero (s1 carries what rounding k lost).
+#include <cooperative_groups.h>
+
 #include "checkpoint.cuh"
+#include "sm100.cuh"
 
 namespace dcn1d {
 
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kRowBytes = 128;                 // a tile's share of one channel's row, at most
+constexpr int kMaxTW = kRowBytes / 2;
+constexpr int kMaxSplit = 8;                   // blocks of a portable cluster
+
+// How a launch cuts [B, C, L] into tiles.
+struct Tiling {
+    int tw, tw_log;    // positions of a tile, a power of two
+    int lpr, lpr_log;  // lanes of a row: tw / V
+    int split;         // blocks that share the channels of a tile (a cluster)
+    int slice;         // channels of a block, a multiple of a warp's rows
+    int64_t tiles;     // tiles of one b
+    int64_t total;     // tiles in all
+};
+
+template <class T> struct Vec {
+    static constexpr int V = 16 / (int)sizeof(T);
+};
+
+template <class T>
+__device__ __forceinline__ void chunk_to_f32(const uint4 &u, float (&f)[Vec<T>::V]) {
+    const T *e = reinterpret_cast<const T *>(&u);
+#pragma unroll
+    for (int j = 0; j < Vec<T>::V; ++j)
+        f[j] = to_f32(e[j]);
+}
+
+template <class T>
+__device__ __forceinline__ uint4 f32_to_chunk(const float (&f)[Vec<T>::V]) {
+    uint4 u;
+    T *e = reinterpret_cast<T *>(&u);
+#pragma unroll
+    for (int j = 0; j < Vec<T>::V; ++j)
+        e[j] = from_f32<T>(f[j]);
+    return u;
+}
+
+// BYTES (4, 8 or 16) from global to shared memory without a register; zeros when !in (the
+// source is then not read).
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *dst, const void *src, bool in) {
+    const int n = in ? BYTES : 0;
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                     "r"(n)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src),
+                     "n"(BYTES), "r"(n)
+                     : "memory");
+}
+
+__device__ __forceinline__ void copies_landed() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Where a thread stands in its block's tile.
+struct Place {
+    int warp, lane, sub, rpw, row;   // rpw: rows of a warp; row: this lane's first row
+    __device__ Place(const Tiling &t) {
+        warp = threadIdx.x / 32;
+        lane = threadIdx.x & 31;
+        sub = lane & (t.lpr - 1);
+        rpw = 32 >> t.lpr_log;
+        row = warp * rpw + (lane >> t.lpr_log);
+    }
+};
+
+// The warp's rows of a block's slice, row by row of `E` values (T, or codes of V bytes a
+// lane): global rows start at src + row * L, shared rows are tw values.  VEC: each lane
+// copies its own chunk (rows are aligned for it and hold whole chunks).  Otherwise lanes
+// run along the values, and the warp meets afterwards.
+template <class E, int V, bool VEC>
+__device__ __forceinline__ void load_rows(E *tile, const E *src, int64_t L, int64_t left, int nrow,
+                                          const Tiling &t, const Place &p) {
+    if constexpr (VEC) {
+        const bool in = p.sub * V < left;
+#pragma unroll 4
+        for (int i = p.row; i < nrow; i += kWarps * p.rpw)
+            copy_async<V * (int)sizeof(E)>(tile + i * t.tw + p.sub * V,
+                                           in ? src + i * L + p.sub * V : src, in);
+    } else {
+        const int n = p.rpw * t.tw;        // values of the warp's rows, 32 or more
+        for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += kWarps * p.rpw)
+#pragma unroll 4
+            for (int e = p.lane; e < n; e += 32) {
+                const int i = i0 + (e >> t.tw_log), col = e & (t.tw - 1);
+                if (i < nrow)
+                    tile[i * t.tw + col] = col < left ? src[i * L + col] : E(0.0f);
+            }
+    }
+}
+
+// The warp's rpw rows at i0 from shared to global memory, values along the lanes.
+template <class E>
+__device__ __forceinline__ void store_rows(const E *tile, E *dst, int64_t L, int64_t left, int i0,
+                                           int nrow, const Tiling &t, const Place &p) {
+    const int n = p.rpw * t.tw;
+    for (int e = p.lane; e < n; e += 32) {
+        const int i = i0 + (e >> t.tw_log), col = e & (t.tw - 1);
+        if (i < nrow && col < left)
+            dst[i * L + col] = tile[i * t.tw + col];
+    }
+}
+
+template <int V> struct CodeWord;
+template <> struct CodeWord<8> { using type = uint2; };
+template <> struct CodeWord<4> { using type = uint32_t; };
+
+// Sums of a group of n values about k.
+struct Moments {
+    float k, s1, s2;
+};
+
+// `count` groups (at(i) and size(i), the first not empty) joined about their common mean,
+// rounded.
+template <int COUNT, class At, class Size>
+__device__ __forceinline__ Moments join(At at, Size size) {
+    const float k0 = at(0).k;
+    float n = 0.0f, sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+        const Moments m = at(i);
+        const float c = size(i);
+        n += c;
+        if (c > 0.0f)
+            sum += fmaf(c, m.k - k0, m.s1);
+    }
+    Moments r{k0 + sum / fmaxf(n, 1.0f), 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+        const Moments m = at(i);
+        const float c = size(i);
+        if (c > 0.0f) {
+            const float d = m.k - r.k;
+            r.s1 += fmaf(c, d, m.s1);
+            r.s2 += fmaf(d, fmaf(c, d, 2.0f * m.s1), m.s2);
+        }
+    }
+    return r;
+}
+
+template <class T, bool VEC, bool CK>
+__global__ void __launch_bounds__(kThreads) norm_tile_kernel(const NormProblem P, const Tiling t) {
+    constexpr int V = Vec<T>::V;
+    extern __shared__ uint4 tile4[];           // [slice][lpr] chunks
+    __shared__ Moments part[kWarps][kMaxTW];   // of a warp's rows, a position
+    __shared__ float count[kWarps];
+    __shared__ Moments own[kMaxTW];            // of the block's rows (cluster)
+    __shared__ float2 stat[kMaxTW];            // (mean, rstd)
+    T *tile = reinterpret_cast<T *>(tile4);
+    const Place p(t);
+    const int rank = blockIdx.x % t.split;
+    const int64_t at = blockIdx.x / t.split;
+    const int64_t b = at / t.tiles, l0 = (at - b * t.tiles) * t.tw;
+    const int64_t left = P.L - l0;             // positions of this tile (tw or more: all)
+    const int c0 = rank * t.slice;
+    const int nrow = min(t.slice, (int)P.C - c0);   // may be 0 or less in the last blocks
+    const int64_t base = (b * P.C + c0) * P.L + l0;
+    load_rows<T, V, VEC>(tile, static_cast<const T *>(P.x) + base, P.L, left, nrow, t, p);
+    copies_landed();
+    __syncwarp();
+
+    float f[V], s[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        s[j] = 0.0f;
+    float n = 0.0f;
+#pragma unroll 2
+    for (int i = p.row; i < nrow; i += kWarps * p.rpw) {
+        chunk_to_f32<T>(tile4[i * t.lpr + p.sub], f);
+        n += 1.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            s[j] += f[j];
+    }
+    for (int o = t.lpr; o < 32; o <<= 1) {
+        n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            s[j] += __shfl_xor_sync(0xFFFFFFFFu, s[j], o);
+    }
+    const float over = n > 0.0f ? 1.0f / n : 0.0f;
+    float mean[V];
+    float s1[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        mean[j] = s[j] * over;
+        s1[j] = s[j] = 0.0f;
+    }
+#pragma unroll 2
+    for (int i = p.row; i < nrow; i += kWarps * p.rpw) {
+        chunk_to_f32<T>(tile4[i * t.lpr + p.sub], f);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float d = f[j] - mean[j];
+            s1[j] += d;
+            s[j] = fmaf(d, d, s[j]);
+        }
+    }
+    for (int o = t.lpr; o < 32; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            s1[j] += __shfl_xor_sync(0xFFFFFFFFu, s1[j], o);
+            s[j] += __shfl_xor_sync(0xFFFFFFFFu, s[j], o);
+        }
+    if (p.lane < t.lpr) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            part[p.warp][p.sub * V + j] = Moments{mean[j], s1[j], s[j]};
+        if (p.lane == 0)
+            count[p.warp] = n;
+    }
+    __syncthreads();
+    const int col = threadIdx.x;
+    Moments m{0.0f, 0.0f, 0.0f};
+    if (col < t.tw) {
+        m = join<kWarps>([&](int w) { return part[w][col]; }, [&](int w) { return count[w]; });
+        own[col] = m;
+    }
+    if (t.split > 1) {
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        if (col < t.tw) {
+            Moments q[kMaxSplit];
+#pragma unroll
+            for (int r = 0; r < kMaxSplit; ++r)
+                q[r] = *cluster.map_shared_rank(&own[col], min(r, t.split - 1));
+            m = join<kMaxSplit>(
+                [&](int r) { return q[r]; },
+                [&](int r) {
+                    return r < t.split ? (float)max(0, min(t.slice, (int)P.C - r * t.slice)) : 0.0f;
+                });
+        }
+    }
+    if (col < t.tw) {
+        const float off = m.s1 / (float)P.C, var = fmaxf(m.s2 / (float)P.C - off * off, 0.0f);
+        const float rstd = 1.0f / sqrtf((m.s2 == m.s2 ? var : m.s2) + P.eps);   // fmaxf drops NaN
+        stat[col] = make_float2(m.k + off, rstd);
+        if (rank == 0 && col < left) {
+            if (P.mean)
+                P.mean[b * P.L + l0 + col] = m.k + off;
+            if (P.rstd)
+                P.rstd[b * P.L + l0 + col] = rstd;
+        }
+    }
+    __syncthreads();
+
+    float rstd[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const float2 q = stat[p.sub * V + j];
+        mean[j] = q.x;
+        rstd[j] = q.y;
+    }
+    const int64_t nb = ck_blocks(P.L);
+    T *y = static_cast<T *>(P.y) + base;
+#pragma unroll 2
+    for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += kWarps * p.rpw) {
+        const int i = i0 + (p.lane >> t.lpr_log);
+        const bool row = i < nrow, in = row && p.sub * V < left;
+        float v[V];
+        chunk_to_f32<T>(tile4[(row ? i : i0) * t.lpr + p.sub], v);
+        const float g = P.gamma && row ? ld_f32(static_cast<const T *>(P.gamma) + c0 + i) : 1.0f;
+        const float be = P.beta && row ? ld_f32(static_cast<const T *>(P.beta) + c0 + i) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            v[j] = (v[j] - mean[j]) * rstd[j];
+            f[j] = fmaf(v[j], g, be);
+        }
+        if constexpr (VEC) {
+            if (in)
+                *reinterpret_cast<uint4 *>(y + i * P.L + p.sub * V) = f32_to_chunk<T>(f);
+        } else {
+            if (row)
+                tile4[i * t.lpr + p.sub] = f32_to_chunk<T>(f);
+            __syncwarp();
+            store_rows(tile, y, P.L, left, i0, nrow, t, p);
+        }
+        if constexpr (CK) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (!row || p.sub * V + j >= left)
+                    v[j] = 0.0f;
+                top = max(top, ck_abs_bits(v[j]));
+            }
+            const int lanes = min(kCkBlock / V, t.lpr);   // lanes of a block of 32 values
+            for (int o = 1; o < lanes; o <<= 1)
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            const uint32_t e = ck_scale(top, ck_top<float>());
+            const float inverse = ck_inverse(e);
+            typename CodeWord<V>::type word;
+            int8_t *q = reinterpret_cast<int8_t *>(&word);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                q[j] = (int8_t)ck_code(v[j], inverse);
+            if constexpr (VEC) {
+                if (in)
+                    *reinterpret_cast<typename CodeWord<V>::type *>(P.codes + base + i * P.L +
+                                                                   p.sub * V) = word;
+            } else {
+                // the rows' bytes over the y that was just stored, one V-byte word a lane
+                __syncwarp();
+                int8_t *rows = reinterpret_cast<int8_t *>(tile + i0 * t.tw);
+                *reinterpret_cast<typename CodeWord<V>::type *>(rows + p.lane * V) = word;
+                __syncwarp();
+                for (int k = p.lane; k < p.rpw * t.tw; k += 32) {
+                    const int ii = i0 + (k >> t.tw_log), col = k & (t.tw - 1);
+                    if (ii < nrow && col < left)
+                        P.codes[base + ii * P.L + col] = rows[k];
+                }
+                __syncwarp();
+            }
+            if (in && (p.sub & (lanes - 1)) == 0)
+                P.scales[(b * P.C + c0 + i) * nb + (l0 + p.sub * V) / kCkBlock] = (uint8_t)e;
+        }
+    }
+    if (t.split > 1)
+        cg::this_cluster().sync();   // another block may still read this one's `own`
+}
+
+// grad_x tile by tile.  A cluster of t.split blocks walks tiles cluster, cluster + n, ...;
+// each row's sums of grad_y v and grad_y over the walk stay in shared memory with the lane
+// that owns the row, and go to the cluster's rows of `part_g` [clusters][2][C] at the end:
+// a fixed order, no atomics.
+template <class T, bool VEC, bool CK>
+__global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormGrad P, const Tiling t,
+                                                                  float *part_g) {
+    constexpr int V = Vec<T>::V;
+    extern __shared__ uint4 tile4[];           // [slice][lpr] chunks of grad_y, then of x / codes
+    __shared__ float2 part[kWarps][kMaxTW];
+    __shared__ float2 own[2][kMaxTW];
+    __shared__ float2 stat[kMaxTW];            // (A, S)
+    T *gtile = reinterpret_cast<T *>(tile4);
+    unsigned char *second = reinterpret_cast<unsigned char *>(tile4 + t.slice * t.lpr);
+    const uint4 *xtile = reinterpret_cast<const uint4 *>(second);
+    int8_t *ctile = reinterpret_cast<int8_t *>(second);
+    float2 *acc = reinterpret_cast<float2 *>(
+        second + (size_t)t.slice * t.tw * (CK ? 1 : sizeof(T)));   // [slice]
+    const Place p(t);
+    const int rank = blockIdx.x % t.split;
+    const int c0 = rank * t.slice;
+    const int nrow = min(t.slice, (int)P.C - c0);
+    const int64_t nb = ck_blocks(P.L);
+    for (int i = p.row; i < nrow; i += kWarps * p.rpw)
+        if (p.sub == 0)
+            acc[i] = make_float2(0.0f, 0.0f);
+    int turn = 0;
+    for (int64_t at = blockIdx.x / t.split; at < t.total; at += gridDim.x / t.split, turn ^= 1) {
+        const int64_t b = at / t.tiles, l0 = (at - b * t.tiles) * t.tw;
+        const int64_t left = P.L - l0;
+        const int64_t base = (b * P.C + c0) * P.L + l0;
+        load_rows<T, V, VEC>(gtile, static_cast<const T *>(P.gy) + base, P.L, left, nrow, t, p);
+        if constexpr (CK)
+            load_rows<int8_t, V, VEC>(ctile, P.codes + base, P.L, left, nrow, t, p);
+        else
+            load_rows<T, V, VEC>(reinterpret_cast<T *>(second), static_cast<const T *>(P.x) + base,
+                                 P.L, left, nrow, t, p);
+        float rstd[V], mean[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const bool in = p.sub * V + j < left;
+            const int64_t l = b * P.L + l0 + p.sub * V + j;
+            rstd[j] = in ? __ldg(P.rstd + l) : 0.0f;
+            mean[j] = !CK && in ? __ldg(P.mean + l) : 0.0f;
+        }
+        const uint8_t *scale = CK ? P.scales + (b * P.C + c0) * nb + (l0 + p.sub * V) / kCkBlock
+                                  : nullptr;
+        auto values = [&](int i, float (&v)[V]) {
+            if constexpr (CK) {
+                const float step = p.sub * V < left ? ck_step(__ldg(scale + i * nb)) : 0.0f;
+                const typename CodeWord<V>::type word =
+                    *reinterpret_cast<const typename CodeWord<V>::type *>(ctile + i * t.tw +
+                                                                         p.sub * V);
+                const int8_t *q = reinterpret_cast<const int8_t *>(&word);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    v[j] = (float)q[j] * step;
+            } else {
+                chunk_to_f32<T>(xtile[i * t.lpr + p.sub], v);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    v[j] = (v[j] - mean[j]) * rstd[j];
+            }
+        };
+        copies_landed();
+        __syncwarp();
+        float a[V], q[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            a[j] = q[j] = 0.0f;
+#pragma unroll 2
+        for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += kWarps * p.rpw) {
+            const int i = i0 + (p.lane >> t.lpr_log);
+            const bool row = i < nrow;
+            float g[V], v[V], sg = 0.0f, sb = 0.0f;
+            if (row) {
+                chunk_to_f32<T>(tile4[i * t.lpr + p.sub], g);
+                values(i, v);
+                const float w = P.gamma ? ld_f32(static_cast<const T *>(P.gamma) + c0 + i) : 1.0f;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float d = w * g[j];
+                    a[j] += d;
+                    q[j] = fmaf(d, v[j], q[j]);
+                    sg = fmaf(g[j], v[j], sg);
+                    sb += g[j];
+                }
+            }
+            if (part_g) {
+                for (int o = 1; o < t.lpr; o <<= 1) {
+                    sg += __shfl_xor_sync(0xFFFFFFFFu, sg, o);
+                    sb += __shfl_xor_sync(0xFFFFFFFFu, sb, o);
+                }
+                if (row && p.sub == 0) {
+                    acc[i].x += sg;
+                    acc[i].y += sb;
+                }
+            }
+        }
+        if (!P.gx) {
+            __syncwarp();   // the next tile's copies overwrite what the warp has read
+            continue;
+        }
+        for (int o = t.lpr; o < 32; o <<= 1)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                a[j] += __shfl_xor_sync(0xFFFFFFFFu, a[j], o);
+                q[j] += __shfl_xor_sync(0xFFFFFFFFu, q[j], o);
+            }
+        if (p.lane < t.lpr)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                part[p.warp][p.sub * V + j] = make_float2(a[j], q[j]);
+        __syncthreads();
+        float2 sum = make_float2(0.0f, 0.0f);
+        if ((int)threadIdx.x < t.tw) {
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                sum.x += part[w][threadIdx.x].x;
+                sum.y += part[w][threadIdx.x].y;
+            }
+            own[turn][threadIdx.x] = sum;
+        }
+        if (t.split > 1) {
+            // `own` alternates: a block writes one half while others may read the other, and
+            // passes the next barrier only after its reads of this one
+            cg::cluster_group cluster = cg::this_cluster();
+            cluster.sync();
+            if ((int)threadIdx.x < t.tw) {
+                sum = make_float2(0.0f, 0.0f);
+                for (int r = 0; r < t.split; ++r) {
+                    const float2 o = *cluster.map_shared_rank(&own[turn][threadIdx.x], r);
+                    sum.x += o.x;
+                    sum.y += o.y;
+                }
+            }
+        }
+        if ((int)threadIdx.x < t.tw)
+            stat[threadIdx.x] = make_float2(sum.x / (float)P.C, sum.y / (float)P.C);
+        __syncthreads();
+        float A[V], S[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float2 o = stat[p.sub * V + j];
+            A[j] = o.x;
+            S[j] = o.y;
+        }
+        T *gx = static_cast<T *>(P.gx) + base;
+#pragma unroll 2
+        for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += kWarps * p.rpw) {
+            const int i = i0 + (p.lane >> t.lpr_log);
+            const bool row = i < nrow;
+            if (row) {
+                float g[V], v[V];
+                chunk_to_f32<T>(tile4[i * t.lpr + p.sub], g);
+                values(i, v);
+                const float w = P.gamma ? ld_f32(static_cast<const T *>(P.gamma) + c0 + i) : 1.0f;
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    g[j] = rstd[j] * (fmaf(w, g[j], -A[j]) - v[j] * S[j]);
+                const uint4 u = f32_to_chunk<T>(g);
+                if constexpr (!VEC)
+                    tile4[i * t.lpr + p.sub] = u;
+                else if (p.sub * V < left)
+                    *reinterpret_cast<uint4 *>(gx + i * P.L + p.sub * V) = u;
+            }
+            if constexpr (!VEC) {
+                __syncwarp();
+                store_rows(gtile, gx, P.L, left, i0, nrow, t, p);
+            }
+        }
+        __syncwarp();
+    }
+    if (part_g) {
+        float *out = part_g + (int64_t)(blockIdx.x / t.split) * 2 * P.C + c0;
+        for (int i = p.row; i < nrow; i += kWarps * p.rpw)
+            if (p.sub == 0) {
+                out[i] = acc[i].x;
+                out[P.C + i] = acc[i].y;
+            }
+    }
+    if (t.split > 1)
+        cg::this_cluster().sync();   // another block may still read this one's `own`
+}
+
+// ---------------------------------------------------------------- rows of C values (L == 1)
+//
+// TPR threads (a warp, or the block) take a row and hold it in registers, NV 16-byte chunks
+// a thread.
+
+// Sum over the TPR threads of a row, in every one of them.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float (&part)[kWarps]) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if constexpr (TPR == kThreads) {
+        __syncthreads();   // the last use of `part` is over
+        if ((threadIdx.x & 31) == 0)
+            part[threadIdx.x / 32] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            v += part[w];
+    }
+    return v;
+}
+
+template <class T, int TPR, int NV>
+__global__ void __launch_bounds__(kThreads) norm_row_kernel(const NormProblem P) {
+    constexpr int V = Vec<T>::V;
+    __shared__ float part[kWarps];
+    const int tid = threadIdx.x % TPR;
+    const int64_t b = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
+    if (b >= P.B)   // whole warps, or (TPR == kThreads) never
+        return;
+    const int C = (int)P.C;
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(P.x) + b * C);
+    uint4 u[NV];
+    float f[V], s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int i = k * TPR + tid;
+        u[k] = i * V < C ? __ldg(x + i) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        chunk_to_f32<T>(u[k], f);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            s += f[j];
+    }
+    const float mean = row_sum<TPR>(s, part) / (float)C;
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        chunk_to_f32<T>(u[k], f);
+        if ((k * TPR + tid) * V < C)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                s = fmaf(f[j] - mean, f[j] - mean, s);
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<TPR>(s, part) / (float)C + P.eps);
+    if (tid == 0) {
+        if (P.mean)
+            P.mean[b] = mean;
+        if (P.rstd)
+            P.rstd[b] = rstd;
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int i = k * TPR + tid;
+        const bool in = i * V < C;
+        float v[V], g[V], be[V];
+        chunk_to_f32<T>(u[k], v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            v[j] = in ? (v[j] - mean) * rstd : 0.0f;
+            g[j] = 1.0f;
+            be[j] = 0.0f;
+        }
+        if (in) {
+            if (P.gamma)
+                chunk_to_f32<T>(__ldg(static_cast<const uint4 *>(P.gamma) + i), g);
+            if (P.beta)
+                chunk_to_f32<T>(__ldg(static_cast<const uint4 *>(P.beta) + i), be);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                f[j] = fmaf(v[j], g[j], be[j]);
+            reinterpret_cast<uint4 *>(static_cast<T *>(P.y) + b * C)[i] = f32_to_chunk<T>(f);
+        }
+        if (P.codes) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                top = max(top, ck_abs_bits(v[j]));
+#pragma unroll
+            for (int o = 1; o < kCkBlock / V; o <<= 1)
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            const uint32_t e = ck_scale(top, ck_top<float>());
+            typename CodeWord<V>::type word;
+            int8_t *q = reinterpret_cast<int8_t *>(&word);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                q[j] = (int8_t)ck_code(v[j], ck_inverse(e));
+            if (in) {
+                reinterpret_cast<typename CodeWord<V>::type *>(P.codes + b * C)[i] = word;
+                if (i * V % kCkBlock == 0)
+                    P.scales[b * ck_blocks(C) + i * V / kCkBlock] = (uint8_t)e;
+            }
+        }
+    }
+}
+
+// A thread keeps the weight gradients of its own channels over the block's rows; the warps
+// of a block add theirs in turn.
+template <class T, int TPR, int NV, bool CK>
+__global__ void __launch_bounds__(kThreads) norm_grad_row_kernel(const NormGrad P, float *part_g) {
+    constexpr int V = Vec<T>::V, RPB = kThreads / TPR;
+    extern __shared__ float sums[];   // [2][C] (TPR < kThreads)
+    __shared__ float part[kWarps];
+    const int tid = threadIdx.x % TPR;
+    const int C = (int)P.C;
+    const int64_t nb = ck_blocks(C);
+    float ag[NV][V], ab[NV][V];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            ag[k][j] = ab[k][j] = 0.0f;
+    for (int64_t b = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; b < P.B;
+         b += (int64_t)gridDim.x * RPB) {
+        const uint4 *gy = reinterpret_cast<const uint4 *>(static_cast<const T *>(P.gy) + b * C);
+        uint4 u[NV], w[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int i = k * TPR + tid;
+            const bool in = i * V < C;
+            u[k] = w[k] = make_uint4(0, 0, 0, 0);
+            if (in)
+                u[k] = __ldg(gy + i);
+            if constexpr (CK) {
+                if (in) {
+                    *reinterpret_cast<typename CodeWord<V>::type *>(&w[k]) =
+                        reinterpret_cast<const typename CodeWord<V>::type *>(P.codes + b * C)[i];
+                    w[k].w = P.scales[b * nb + i * V / kCkBlock];
+                }
+            } else if (in) {
+                w[k] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(P.x) + b * C) + i);
+            }
+        }
+        const float rstd = P.rstd[b], mean = CK ? 0.0f : P.mean[b];
+        auto load = [&](int k, float (&g)[V], float (&v)[V], float (&d)[V]) {
+            const int i = k * TPR + tid;
+            const bool in = i * V < C;
+            chunk_to_f32<T>(u[k], g);
+            if constexpr (CK) {
+                const int8_t *q = reinterpret_cast<const int8_t *>(&w[k]);
+                const float step = ck_step(w[k].w);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    v[j] = (float)q[j] * step;
+            } else {
+                chunk_to_f32<T>(w[k], v);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    v[j] = in ? (v[j] - mean) * rstd : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                d[j] = 1.0f;
+            if (P.gamma && in)
+                chunk_to_f32<T>(__ldg(static_cast<const uint4 *>(P.gamma) + i), d);
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                d[j] *= g[j];
+        };
+        float a = 0.0f, q = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float g[V], v[V], d[V];
+            load(k, g, v, d);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                a += d[j];
+                q = fmaf(d[j], v[j], q);
+                ag[k][j] = fmaf(g[j], v[j], ag[k][j]);
+                ab[k][j] += g[j];
+            }
+        }
+        if (P.gx) {
+            const float A = row_sum<TPR>(a, part) / (float)C;
+            const float S = row_sum<TPR>(q, part) / (float)C;
+            uint4 *gx = reinterpret_cast<uint4 *>(static_cast<T *>(P.gx) + b * C);
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float g[V], v[V], d[V];
+                load(k, g, v, d);
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    d[j] = rstd * (d[j] - A - v[j] * S);
+                if ((k * TPR + tid) * V < C)
+                    gx[k * TPR + tid] = f32_to_chunk<T>(d);
+            }
+        }
+    }
+    if (!part_g)
+        return;
+    float *out = part_g + (int64_t)blockIdx.x * 2 * C;
+    float *to = TPR == kThreads ? out : sums;
+    for (int r = 0; r < RPB; ++r) {
+        if ((int)threadIdx.x / TPR == r)
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int i = k * TPR + tid;
+                if (i * V < C)
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const int c = i * V + j;
+                        to[c] = r == 0 ? ag[k][j] : to[c] + ag[k][j];
+                        to[C + c] = r == 0 ? ab[k][j] : to[C + c] + ab[k][j];
+                    }
+            }
+        __syncthreads();
+    }
+    if (TPR < kThreads)
+        for (int c = threadIdx.x; c < 2 * C; c += kThreads)
+            out[c] = sums[c];
+}
+
+// ---------------------------------------------------------------- any sizes
+//
+// For channel counts past what a cluster holds, and unaligned rows of single tokens: the
+// values are read again (from the L2) in each pass.  A block takes TL consecutive positions
+// of one b, lanes along them, so a warp covers 32 / TL channels; with L == 1 the lanes run
+// along the channels.
 
 // Sums `v` over the lanes of a warp that hold the same position, then over the warps:
 // every thread of the block gets the total of its own position.
@@ -156,16 +907,26 @@ __global__ void __launch_bounds__(kThreads) norm_grad_any_kernel(const NormGrad 
     }
 }
 
-// grad_gamma[c] and grad_beta[c]: the blocks' partial sums in block order.
+// grad_gamma[c] and grad_beta[c]: the blocks' partial sums, eight interleaved chains joined
+// in order.
 template <class T>
 __global__ void __launch_bounds__(256) norm_weight_grad_kernel(const float *part, int64_t n,
                                                                int64_t C, T *ggamma, T *gbeta) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= 2 * C)
-        return;
+    __shared__ float sums[8][33];
+    const int lane = threadIdx.x & 31, group = threadIdx.x / 32;
+    const int64_t i = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.0f;
-    for (int64_t j = 0; j < n; ++j)
-        s += part[j * 2 * C + i];
+    if (i < 2 * C)
+#pragma unroll 4
+        for (int64_t j = group; j < n; j += 8)
+            s += part[j * 2 * C + i];
+    sums[group][lane] = s;
+    __syncthreads();
+    if (group > 0 || i >= 2 * C)
+        return;
+#pragma unroll
+    for (int g = 1; g < 8; ++g)
+        s += sums[g][lane];
     T *out = i < C ? ggamma : gbeta;
     if (out)
         out[i < C ? i : i - C] = from_f32<T>(s);
@@ -178,35 +939,202 @@ int lanes_along(int64_t L) {
     return TL;
 }
 
-int64_t grad_tiles(const NormGrad &P) {
-    const int TL = lanes_along(P.L);
-    return P.B * ((P.L + TL - 1) / TL);
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Tiles of [B, C, L] for `bytes` of shared memory a value and `extra` a channel; false when
+// a cluster cannot hold the channels of a tile.
+//
+// A block's share is at most a third of an SM's shared memory, so that three blocks are
+// there to load, reduce and store at different times; channels past that are split over a
+// cluster, and so are the channels of a tile where there are too few tiles for the SMs (at
+// least 32 channels a block, four rows a warp).
+bool make_tiling(int64_t B, int64_t C, int64_t L, int size, int bytes, int extra, Tiling *t) {
+    const int V = 16 / size;
+    if (L < 2)
+        return false;
+    t->tw = V;
+    while (t->tw < kRowBytes / size && t->tw < L)
+        t->tw *= 2;
+    t->lpr = t->tw / V;
+    t->tw_log = __builtin_ctz(t->tw);
+    t->lpr_log = __builtin_ctz(t->lpr);
+    const int rpw = 32 / t->lpr;
+    t->tiles = (L + t->tw - 1) / t->tw;
+    t->total = B * t->tiles;
+    auto slice = [&](int split) { return ((C + split - 1) / split + rpw - 1) / rpw * rpw; };
+    auto shared = [&](int split) { return slice(split) * (t->tw * bytes + extra); };
+    t->split = 1;
+    while (t->split < kMaxSplit && shared(t->split) > 70 * 1024)
+        t->split *= 2;
+    if (shared(t->split) > 200 * 1024)
+        return false;
+    while (t->split < kMaxSplit && t->total * t->split < sm_count_or(148) &&
+           slice(t->split) >= 2 * kWarps * rpw)
+        t->split *= 2;
+    t->slice = (int)slice(t->split);
+    return t->total * t->split < (1LL << 31);
 }
 
-int64_t grad_blocks(const NormGrad &P) {
-    const int64_t most = (int64_t)sm_count_or(148) * 8, n = grad_tiles(P);
-    return n < most ? n : most;
+// Blocks of a tile kernel that one SM holds.
+int blocks_per_sm(size_t shared) {
+    const int n = (int)((227 * 1024) / (shared + 8 * 1024));   // 8 KB: static and reserved
+    return n < 1 ? 1 : n > 6 ? 6 : n;
+}
+
+template <class... A>
+cudaError_t launch_cluster(void (*kernel)(A...), unsigned grid, unsigned split, size_t shared,
+                           cudaStream_t s, A... args) {
+    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kernel), (int)shared);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = shared;
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = split;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Chunks a thread holds of a row of C values, for 32 and for kThreads threads a row: 1, 2
+// or 4, else 0.
+int row_chunks(int64_t C, int V, int threads) {
+    const int64_t n = (C + (int64_t)threads * V - 1) / ((int64_t)threads * V);
+    return n == 1 ? 1 : n == 2 ? 2 : n <= 4 ? 4 : 0;
+}
+
+template <class T>
+cudaError_t norm(const NormProblem &P, cudaStream_t s) {
+    constexpr int V = Vec<T>::V;
+    const bool base = aligned(P.x, 16) && aligned(P.y, 16) && aligned(P.codes, V);
+    if (P.L == 1 && base && P.C % V == 0 && aligned(P.gamma, 16) && aligned(P.beta, 16)) {
+        const int warp = row_chunks(P.C, V, 32), block = row_chunks(P.C, V, kThreads);
+        const unsigned gw = (unsigned)((P.B + kWarps - 1) / kWarps), gb = (unsigned)P.B;
+        if (warp == 1)
+            norm_row_kernel<T, 32, 1><<<gw, kThreads, 0, s>>>(P);
+        else if (warp == 2)
+            norm_row_kernel<T, 32, 2><<<gw, kThreads, 0, s>>>(P);
+        else if (warp == 4)
+            norm_row_kernel<T, 32, 4><<<gw, kThreads, 0, s>>>(P);
+        else if (block == 1)
+            norm_row_kernel<T, kThreads, 1><<<gb, kThreads, 0, s>>>(P);
+        else if (block == 2)
+            norm_row_kernel<T, kThreads, 2><<<gb, kThreads, 0, s>>>(P);
+        else if (block == 4)
+            norm_row_kernel<T, kThreads, 4><<<gb, kThreads, 0, s>>>(P);
+        if (warp || block)
+            return cudaGetLastError();
+    }
+    Tiling t;
+    if (make_tiling(P.B, P.C, P.L, sizeof(T), sizeof(T), 0, &t)) {
+        const unsigned grid = (unsigned)(t.total * t.split);
+        const size_t shared = (size_t)t.slice * t.tw * sizeof(T);
+        const bool vec = base && P.L % V == 0;
+        auto kernel = vec ? (P.codes ? norm_tile_kernel<T, true, true> : norm_tile_kernel<T, true, false>)
+                          : (P.codes ? norm_tile_kernel<T, false, true> : norm_tile_kernel<T, false, false>);
+        return launch_cluster(kernel, grid, (unsigned)t.split, shared, s, P, t);
+    }
+    const int TL = lanes_along(P.L);
+    norm_any_kernel<T><<<(unsigned)(P.B * ((P.L + TL - 1) / TL)), kThreads, 0, s>>>(P, TL);
+    return cudaGetLastError();
+}
+
+// How a backward runs: the kernel family, its blocks, and the rows of partial sums.
+struct GradPlan {
+    int kind;          // 0: any sizes, 1: tiles, 2: a warp a row, 3: a block a row
+    int nv;
+    bool vec;
+    Tiling t;
+    size_t shared;
+    int64_t blocks, rows;
+};
+
+template <class T>
+GradPlan grad_plan(const NormGrad &P) {
+    constexpr int V = Vec<T>::V;
+    GradPlan g = {};
+    const int sms = sm_count_or(148);
+    const bool base = aligned(P.gy, 16) && aligned(P.gx, 16) &&
+                      (P.from_codes ? aligned(P.codes, V) : aligned(P.x, 16));
+    if (P.B == 0 || P.L == 0)
+        return g;
+    if (P.L == 1 && base && P.C % V == 0 && aligned(P.gamma, 16)) {
+        const int warp = row_chunks(P.C, V, 32), block = row_chunks(P.C, V, kThreads);
+        if (warp || block) {
+            g.kind = warp ? 2 : 3;
+            g.nv = warp ? warp : block;
+            g.shared = warp ? 2 * P.C * sizeof(float) : 0;
+            const int64_t need = warp ? (P.B + kWarps - 1) / kWarps : P.B;
+            g.blocks = g.rows = need < 2 * sms ? need : 2 * sms;
+            return g;
+        }
+    }
+    const int second = P.from_codes ? 1 : (int)sizeof(T);
+    if (make_tiling(P.B, P.C, P.L, sizeof(T), (int)sizeof(T) + second, sizeof(float2), &g.t)) {
+        g.kind = 1;
+        g.vec = base && P.L % V == 0;
+        g.shared = (size_t)g.t.slice * (g.t.tw * (sizeof(T) + second) + sizeof(float2));
+        const int64_t room = (int64_t)sms * blocks_per_sm(g.shared) / g.t.split;
+        g.rows = g.t.total < room ? g.t.total : room;
+        g.blocks = g.rows * g.t.split;
+        return g;
+    }
+    const int TL = lanes_along(P.L);
+    const int64_t n = P.B * ((P.L + TL - 1) / TL), most = (int64_t)sms * 8;
+    g.blocks = g.rows = n < most ? n : most;
+    return g;
+}
+
+template <class T, bool CK>
+cudaError_t run_norm_grad(const NormGrad &P, const GradPlan &g, float *part, cudaStream_t s) {
+    const unsigned grid = (unsigned)g.blocks;
+    if (g.kind == 1)
+        return launch_cluster(g.vec ? norm_grad_tile_kernel<T, true, CK>
+                                    : norm_grad_tile_kernel<T, false, CK>,
+                              grid, (unsigned)g.t.split, g.shared, s, P, g.t, part);
+    if (g.kind >= 2) {
+        auto kernel = g.kind == 2 ? (g.nv == 1   ? norm_grad_row_kernel<T, 32, 1, CK>
+                                     : g.nv == 2 ? norm_grad_row_kernel<T, 32, 2, CK>
+                                                 : norm_grad_row_kernel<T, 32, 4, CK>)
+                                  : (g.nv == 1   ? norm_grad_row_kernel<T, kThreads, 1, CK>
+                                     : g.nv == 2 ? norm_grad_row_kernel<T, kThreads, 2, CK>
+                                                 : norm_grad_row_kernel<T, kThreads, 4, CK>);
+        return launch_cluster(kernel, grid, 1u, g.shared, s, P, part);
+    }
+    const int TL = lanes_along(P.L);
+    norm_grad_any_kernel<T, CK>
+        <<<grid, kThreads, 0, s>>>(P, TL, P.B * ((P.L + TL - 1) / TL), part);
+    return cudaGetLastError();
 }
 
 template <class T>
 cudaError_t norm_grad(const NormGrad &P, void *ws, cudaStream_t s, int *launches) {
-    const int64_t n = grad_tiles(P), blocks = grad_blocks(P);
+    const GradPlan g = grad_plan<T>(P);
     const bool weights = P.ggamma || P.gbeta;
     float *part = weights ? static_cast<float *>(ws) : nullptr;   // NULL for an empty input
-    if (n > 0 && (P.gx || weights)) {
-        const int TL = lanes_along(P.L);
-        if (P.from_codes)
-            norm_grad_any_kernel<T, true><<<(unsigned)blocks, kThreads, 0, s>>>(P, TL, n, part);
-        else
-            norm_grad_any_kernel<T, false><<<(unsigned)blocks, kThreads, 0, s>>>(P, TL, n, part);
+    if (g.blocks > 0 && (P.gx || weights)) {
+        const cudaError_t e = P.from_codes ? run_norm_grad<T, true>(P, g, part, s)
+                                           : run_norm_grad<T, false>(P, g, part, s);
+        if (e != cudaSuccess)
+            return e;
         ++*launches;
     }
     if (weights) {
-        norm_weight_grad_kernel<T><<<(unsigned)((2 * P.C + 255) / 256), 256, 0, s>>>(
-            part, n > 0 ? blocks : 0, P.C, static_cast<T *>(P.ggamma), static_cast<T *>(P.gbeta));
+        norm_weight_grad_kernel<T><<<(unsigned)((2 * P.C + 31) / 32), 256, 0, s>>>(
+            part, g.rows, P.C, static_cast<T *>(P.ggamma), static_cast<T *>(P.gbeta));
         ++*launches;
     }
     return cudaGetLastError();
+}
+
+template <class T>
+size_t grad_workspace(const NormGrad &P) {
+    return (size_t)grad_plan<T>(P).rows * 2 * P.C * sizeof(float);
 }
 
 }  // namespace
@@ -217,19 +1145,21 @@ bool norm_grid_ok(int64_t B, int64_t L) {
 }
 
 cudaError_t launch_norm(const NormProblem &P, cudaStream_t s) {
-    const int TL = lanes_along(P.L);
-    const unsigned grid = (unsigned)(P.B * ((P.L + TL - 1) / TL));
     if (P.dtype == DCN1D_BF16)
-        norm_any_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(P, TL);
-    else if (P.dtype == DCN1D_F16)
-        norm_any_kernel<__half><<<grid, kThreads, 0, s>>>(P, TL);
-    else
-        norm_any_kernel<float><<<grid, kThreads, 0, s>>>(P, TL);
-    return cudaGetLastError();
+        return norm<__nv_bfloat16>(P, s);
+    if (P.dtype == DCN1D_F16)
+        return norm<__half>(P, s);
+    return norm<float>(P, s);
 }
 
 size_t norm_grad_workspace(const NormGrad &P) {
-    return P.ggamma || P.gbeta ? (size_t)grad_blocks(P) * 2 * P.C * sizeof(float) : 0;
+    if (!P.ggamma && !P.gbeta)
+        return 0;
+    if (P.dtype == DCN1D_BF16)
+        return grad_workspace<__nv_bfloat16>(P);
+    if (P.dtype == DCN1D_F16)
+        return grad_workspace<__half>(P);
+    return grad_workspace<float>(P);
 }
 
 cudaError_t launch_norm_grad(const NormGrad &P, void *ws, cudaStream_t s, int *launches) {
