@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 from typing import NamedTuple
 
@@ -96,15 +97,16 @@ SIGNATURES = [
      [_T, _T, _T, _T, _T] + [_I64] * 6 + [_INT] + [_T] * 5),
     ("dcn1d_test_forward_stalled", _INT,
      [_T, _T, _T, _I64, _I64, _I64, _I64, _I64, _INT, _T, _I64, _P]),
-    ("dcn1d_layer_norm_forward", _INT, [_T] * 3 + [ctypes.c_float] + [_T] * 5 + [_P]),
-    ("dcn1d_layer_norm_backward_workspace_size", _I64, [_T] * 10),
-    ("dcn1d_layer_norm_backward", _INT, [_T] * 10 + [_P, ctypes.c_size_t, _P]),
-    ("dcn1d_checkpoint_pack", _INT, [_T] * 3 + [_P]),
-    ("dcn1d_checkpoint_unpack", _INT, [_T] * 5 + [_P]),
+    # descriptors as plain addresses (see _pack)
+    ("dcn1d_layer_norm_forward", _INT, [_P] * 3 + [ctypes.c_float] + [_P] * 6),
+    ("dcn1d_layer_norm_backward_workspace_size", _I64, [_P] * 10),
+    ("dcn1d_layer_norm_backward", _INT, [_P] * 11 + [ctypes.c_size_t, _P]),
+    ("dcn1d_checkpoint_pack", _INT, [_P] * 4),
+    ("dcn1d_checkpoint_unpack", _INT, [_P] * 6),
     ("dcn1d_backward_checkpoint_workspace_size", _I64,
-     [_T] * 8 + [_I64] * 6 + [_INT] + [_T] * 5),
+     [_P] * 8 + [_I64] * 6 + [_INT] + [_P] * 5),
     ("dcn1d_backward_checkpoint", _INT,
-     [_T] * 8 + [_I64] * 6 + [_INT] + [_T] * 5 + [_P, ctypes.c_size_t, _P]),
+     [_P] * 8 + [_I64] * 6 + [_INT] + [_P] * 6 + [ctypes.c_size_t, _P]),
 ]
 
 
@@ -649,16 +651,62 @@ def _empty_checkpoint(shape, dev):
                        torch.empty(_scales_shape(*shape), dtype=torch.uint8, device=dev))
 
 
+_PACK = struct.Struct("@Pii4q").pack_into       # a dcn1d_tensor
+_DESC_BYTES = ctypes.sizeof(Dcn1dTensor)
+_NO_SIZES = tuple((0,) * (4 - n) for n in range(5))
+
+
+def _pack(tensors):
+    """(keep, addresses): descriptors of contiguous tensors (None -> None) in one block of
+    memory that lives as long as ``keep``.  A third of the cost of a ctypes structure each,
+    which is what a small call spends most of its time on."""
+    keep = bytearray(_DESC_BYTES * len(tensors))
+    at = ctypes.addressof(ctypes.c_char.from_buffer(keep))
+    out = []
+    off = 0
+    for t in tensors:
+        if t is None:
+            out.append(None)
+        else:
+            shape = t.shape
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
+            n = len(shape)
+            if n > 4:
+                raise ValueError("at most 4 dimensions")
+            _PACK(keep, off, t.data_ptr(), _DTYPES.get(t.dtype, _BAD_DTYPE), n, *shape,
+                  *_NO_SIZES[n])
+            out.append(at + off)
+        off += _DESC_BYTES
+    return keep, out
+
+
+def _device_index(tensors):
+    """The CUDA device that all tensors are on."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError("every tensor must be on a CUDA device")
+            if dev < 0:
+                dev = d
+            elif d != dev:
+                raise ValueError("every tensor must be on the same CUDA device")
+    return dev
+
+
 def _on(dev, stream):
-    """Context in which a call's tensors are allocated and its work is enqueued: the given
-    stream (memory allocated here then belongs to it), else the device's current one."""
+    """(context, raw stream) in which a call's tensors are allocated and its work enqueued:
+    the given stream (memory allocated there then belongs to it), else the device's current
+    one."""
     if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
-        return torch.cuda.stream(stream)
-    if torch.cuda.current_device() == dev.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+        if stream.device.index != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{dev}")
+        return torch.cuda.stream(stream), stream.cuda_stream
+    ctx = (contextlib.nullcontext() if torch.cuda.current_device() == dev
+           else torch.cuda.device(dev))
+    return ctx, torch.cuda.current_stream(dev).cuda_stream
 
 
 def _check_status(st, where):
@@ -666,17 +714,19 @@ def _check_status(st, where):
         raise Dcn1dError(st, where)
 
 
-def _workspace(need, workspace, dev, where):
-    """(pointer, bytes, tensor) of a call's scratch of ``need`` bytes."""
+def _workspace(need, workspace, like, where):
+    """(tensor, pointer, bytes) of a call's scratch of ``need`` bytes on the device of
+    ``like``."""
     if need < 0:
         raise Dcn1dError(-need, where + "_workspace_size")
     if need == 0:
-        return None, 0, None
+        return None, None, 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    if workspace.device != dev or workspace.dtype != torch.uint8 or workspace.numel() < need:
-        raise ValueError(f"workspace must be a uint8 tensor of >= {need} bytes on {dev}")
-    return workspace.data_ptr(), workspace.numel(), workspace
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif (workspace.device != like.device or workspace.dtype != torch.uint8
+          or workspace.numel() < need or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a uint8 tensor of >= {need} bytes on {like.device}")
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def dcn1d_layer_norm_forward(x, gamma=None, beta=None, eps=1e-5, stats=True, checkpoint=None,
@@ -689,26 +739,33 @@ def dcn1d_layer_norm_forward(x, gamma=None, beta=None, eps=1e-5, stats=True, che
     and dcn1d_backward_checkpoint; None otherwise.  ``out`` receives y when given.  Runs on
     ``stream`` (default: the current torch stream of x's device); does not synchronise.
     """
-    given = checkpoint if isinstance(checkpoint, tuple) else (None, None)
-    dev = _check_device((x, gamma, beta, out, *given))
+    codes, scales = checkpoint if isinstance(checkpoint, tuple) else (None, None)
+    dev = _device_index((x, gamma, beta, out, codes, scales))
     lib = load()
-    with _on(dev, stream):
+    ctx, raw = _on(dev, stream)
+    with ctx:
         if out is None:
             out = torch.empty_like(x)
-        mean = rstd = None
-        if stats:
-            B, _, L = x.shape
-            mean, rstd = torch.empty((2, B, L), dtype=torch.float32, device=dev)
-        kept = Checkpoint8(*given) if given[0] is not None else None
-        if kept is None and checkpoint:
-            kept = _empty_checkpoint(x.shape, dev)
-        refs = [_ref(_desc(t)) for t in (x, gamma, beta, out, mean, rstd, *(kept or given))]
-        st = lib.dcn1d_layer_norm_forward(*refs[:3], eps, *refs[3:], _P(_stream_ptr(stream, dev)))
+        mean = rstd = kept = None
+        if stats and x.ndim == 3:
+            size = (x.shape[0], x.shape[2])
+            mean = torch.empty(size, dtype=torch.float32, device=x.device)
+            rstd = torch.empty(size, dtype=torch.float32, device=x.device)
+        if codes is not None:
+            kept = Checkpoint8(codes, scales)
+        elif checkpoint:
+            kept = _empty_checkpoint(x.shape, x.device)
+            codes, scales = kept
+        keep, d = _pack((x, gamma, beta, out, mean, rstd, codes, scales))
+        st = lib.dcn1d_layer_norm_forward(d[0], d[1], d[2], eps, d[3], d[4], d[5], d[6], d[7],
+                                          raw)
     _check_status(st, "dcn1d_layer_norm_forward")
     return out, mean, rstd, kept
 
 
 NORM_GRADS = ("x", "gamma", "beta")
+_NORM_GRADS = frozenset(NORM_GRADS)
+_norm_need = {}   # scratch bytes of the layer norm backward by what they depend on
 
 
 def dcn1d_layer_norm_backward(x, gamma, mean, rstd, grad_y, wanted=NORM_GRADS, grads=None,
@@ -722,24 +779,32 @@ def dcn1d_layer_norm_backward(x, gamma, mean, rstd, grad_y, wanted=NORM_GRADS, g
     are allocated with torch unless a uint8 CUDA tensor ``workspace`` is given.  Runs on
     ``stream``; does not synchronise.
     """
-    unknown = set(wanted) - set(NORM_GRADS)
-    if unknown:
-        raise ValueError(f"unknown gradients {sorted(unknown)}")
+    if not _NORM_GRADS.issuperset(wanted):
+        raise ValueError(f"unknown gradients {sorted(set(wanted) - _NORM_GRADS)}")
     codes, scales = x if isinstance(x, tuple) else (None, None)
     x = None if codes is not None else x
-    res = {n: (grads or {}).get(n) for n in wanted}
-    dev = _check_device((grad_y, x, gamma, mean, rstd, codes, scales, *res.values()))
+    res = {n: grads.get(n) for n in wanted} if grads else dict.fromkeys(wanted)
+    dev = _device_index((grad_y, x, gamma, mean, rstd, codes, scales, *res.values()))
     lib = load()
-    with _on(dev, stream):
-        for n in wanted:
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        shape = grad_y.shape
+        for n in res:
             if res[n] is None:
-                res[n] = torch.empty(grad_y.shape if n == "x" else grad_y.shape[1:2],
-                                     dtype=grad_y.dtype, device=dev)
-        refs = [_ref(_desc(t)) for t in (x, gamma, mean, rstd, codes, scales, grad_y,
-                                         *(res.get(n) for n in NORM_GRADS))]
-        need = int(lib.dcn1d_layer_norm_backward_workspace_size(*refs))
-        ptr, size, workspace = _workspace(need, workspace, dev, "dcn1d_layer_norm_backward")
-        st = lib.dcn1d_layer_norm_backward(*refs, _P(ptr), size, _P(_stream_ptr(stream, dev)))
+                res[n] = torch.empty(shape if n == "x" else shape[1:2], dtype=grad_y.dtype,
+                                     device=grad_y.device)
+        keep, d = _pack((x, gamma, mean, rstd, codes, scales, grad_y, res.get("x"),
+                         res.get("gamma"), res.get("beta")))
+        key = (dev, shape, grad_y.dtype, x is None, d[8] is None and d[9] is None)
+        need = _norm_need.get(key)
+        if need is None:
+            need = int(lib.dcn1d_layer_norm_backward_workspace_size(*d))
+            if need >= 0:
+                if len(_norm_need) > 4096:
+                    _norm_need.clear()
+                _norm_need[key] = need
+        workspace, ptr, size = _workspace(need, workspace, grad_y, "dcn1d_layer_norm_backward")
+        st = lib.dcn1d_layer_norm_backward(*d, ptr, size, raw)
     _check_status(st, "dcn1d_layer_norm_backward")
     return res
 
@@ -747,12 +812,13 @@ def dcn1d_layer_norm_backward(x, gamma, mean, rstd, grad_y, wanted=NORM_GRADS, g
 def dcn1d_checkpoint_pack(x, out=None, stream=None):
     """x [B, C, L] in 8 bits a value: a Checkpoint8 (``out`` when given).  Does not
     synchronise."""
-    dev = _check_device((x, *(out or ())))
+    dev = _device_index((x, *(out or ())))
     lib = load()
-    with _on(dev, stream):
-        kept = Checkpoint8(*out) if out is not None else _empty_checkpoint(x.shape, dev)
-        refs = [_ref(_desc(t)) for t in (x, *kept)]
-        st = lib.dcn1d_checkpoint_pack(*refs, _P(_stream_ptr(stream, dev)))
+    ctx, raw = _on(dev, stream)
+    with ctx:
+        kept = Checkpoint8(*out) if out is not None else _empty_checkpoint(x.shape, x.device)
+        keep, d = _pack((x, *kept))
+        st = lib.dcn1d_checkpoint_pack(*d, raw)
     _check_status(st, "dcn1d_checkpoint_pack")
     return kept
 
@@ -763,13 +829,14 @@ def dcn1d_checkpoint_unpack(checkpoint, gamma=None, beta=None, dtype=torch.float
     gamma * value + beta with ``gamma`` and ``beta`` [C] of that dtype, else the values
     themselves.  Does not synchronise."""
     codes, scales = checkpoint
-    dev = _check_device((codes, scales, gamma, beta, out))
+    dev = _device_index((codes, scales, gamma, beta, out))
     lib = load()
-    with _on(dev, stream):
+    ctx, raw = _on(dev, stream)
+    with ctx:
         if out is None:
-            out = torch.empty(codes.shape, dtype=dtype, device=dev)
-        refs = [_ref(_desc(t)) for t in (codes, scales, gamma, beta, out)]
-        st = lib.dcn1d_checkpoint_unpack(*refs, _P(_stream_ptr(stream, dev)))
+            out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+        keep, d = _pack((codes, scales, gamma, beta, out))
+        st = lib.dcn1d_checkpoint_unpack(*d, raw)
     _check_status(st, "dcn1d_checkpoint_unpack")
     return out
 
@@ -791,22 +858,22 @@ def dcn1d_backward_checkpoint(checkpoint, offsets, mask, weight, grad_out, strid
         raise ValueError(f"unknown gradients {sorted(unknown)}")
     codes, scales = checkpoint
     res = {n: (grads or {}).get(n) for n in wanted}
-    dev = _check_device((grad_out, codes, scales, gamma, beta, offsets, mask, weight,
+    dev = _device_index((grad_out, codes, scales, gamma, beta, offsets, mask, weight,
                          *res.values()))
     lib = load()
     pl, pr = resolve_padding(padding, weight.shape[2], stride, dilation)
     args = (stride, pl, pr, dilation, groups, offset_groups, int(bool(unconstrained)))
-    with _on(dev, stream):
+    ctx, raw = _on(dev, stream)
+    with ctx:
         shapes = {"x": codes.shape, "offsets": offsets.shape, "weight": weight.shape,
                   "mask": offsets.shape, "bias": weight.shape[:1]}
         for n in wanted:
             if res[n] is None:
-                res[n] = torch.empty(shapes[n], dtype=grad_out.dtype, device=dev)
-        refs = [_ref(_desc(t)) for t in (codes, scales, gamma, beta, offsets, mask, weight,
-                                         grad_out, *(res.get(n) for n in GRADS))]
-        need = int(lib.dcn1d_backward_checkpoint_workspace_size(*refs[:8], *args, *refs[8:]))
-        ptr, size, workspace = _workspace(need, workspace, dev, "dcn1d_backward_checkpoint")
-        st = lib.dcn1d_backward_checkpoint(*refs[:8], *args, *refs[8:], _P(ptr), size,
-                                           _P(_stream_ptr(stream, dev)))
+                res[n] = torch.empty(shapes[n], dtype=grad_out.dtype, device=grad_out.device)
+        keep, d = _pack((codes, scales, gamma, beta, offsets, mask, weight, grad_out,
+                         *(res.get(n) for n in GRADS)))
+        need = int(lib.dcn1d_backward_checkpoint_workspace_size(*d[:8], *args, *d[8:]))
+        workspace, ptr, size = _workspace(need, workspace, grad_out, "dcn1d_backward_checkpoint")
+        st = lib.dcn1d_backward_checkpoint(*d[:8], *args, *d[8:], ptr, size, raw)
     _check_status(st, "dcn1d_backward_checkpoint")
     return res

@@ -53,6 +53,24 @@ __device__ __forceinline__ int ck_code(float v, float inverse) {
 // The step itself; infinity for s = 255 (code 0 times infinity is NaN).
 __device__ __forceinline__ float ck_step(uint32_t s) { return __uint_as_float(s << 23); }
 
+// 1.5 * 2^23: a float near it steps by one, so v / step + kCkRound is v / step rounded to an
+// integer (ties to even), whose low byte is the code.
+constexpr float kCkRound = 12582912.0f;
+// 2^23 + 128: the float with the bits 0x4B0000xx is 2^23 + xx, so with xx = code + 128 (the
+// code's sign bit flipped) subtracting this gives the code.
+constexpr float kCkBias = 8388736.0f;
+
+// Four codes (a word whose sign bits are flipped) as 2^23 + 128 + code.
+__device__ __forceinline__ float ck_biased(uint32_t flipped, int j) {
+    return __uint_as_float(__byte_perm(flipped, 0x4B000000u, 0x7540 + j));
+}
+
+// The low bytes of four floats as one word.
+__device__ __forceinline__ uint32_t ck_low_bytes(float a, float b, float c, float d) {
+    return __byte_perm(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040),
+                       __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040), 0x5410);
+}
+
 // Blocks of a row of n values.
 __host__ __device__ __forceinline__ int64_t ck_blocks(int64_t n) {
     return (n + kCkBlock - 1) / kCkBlock;

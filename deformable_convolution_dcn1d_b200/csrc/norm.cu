@@ -21,6 +21,7 @@
 #include <cooperative_groups.h>
 
 #include "checkpoint.cuh"
+#include "pairs.cuh"
 #include "sm100.cuh"
 
 namespace dcn1d {
@@ -42,10 +43,6 @@ struct Tiling {
     int slice;         // channels of a block, a multiple of a warp's rows
     int64_t tiles;     // tiles of one b
     int64_t total;     // tiles in all
-};
-
-template <class T> struct Vec {
-    static constexpr int V = 16 / (int)sizeof(T);
 };
 
 template <class T>
@@ -97,19 +94,24 @@ struct Place {
     }
 };
 
-// The warp's rows of a block's slice, row by row of `E` values (T, or codes of V bytes a
-// lane): global rows start at src + row * L, shared rows are tw values.  VEC: each lane
-// copies its own chunk (rows are aligned for it and hold whole chunks).  Otherwise lanes
-// run along the values, and the warp meets afterwards.
+// The warp's rows of a block's slice, `E` values (T, or codes): global rows start at
+// src + row * L, shared rows are tw values.  VEC: each lane copies its own chunk (rows are
+// aligned for it and hold whole chunks).  Otherwise lanes run along the values, and the
+// warp meets afterwards.
 template <class E, int V, bool VEC>
 __device__ __forceinline__ void load_rows(E *tile, const E *src, int64_t L, int64_t left, int nrow,
                                           const Tiling &t, const Place &p) {
     if constexpr (VEC) {
         const bool in = p.sub * V < left;
+        const E *from = in ? src + p.row * L + p.sub * V : src;
+        const int64_t step = in ? (int64_t)kWarps * p.rpw * L : 0;
+        E *to = tile + p.row * t.tw + p.sub * V;
 #pragma unroll 4
-        for (int i = p.row; i < nrow; i += kWarps * p.rpw)
-            copy_async<V * (int)sizeof(E)>(tile + i * t.tw + p.sub * V,
-                                           in ? src + i * L + p.sub * V : src, in);
+        for (int i = p.row; i < nrow; i += kWarps * p.rpw) {
+            copy_async<V * (int)sizeof(E)>(to, from, in);
+            from += step;
+            to += (kWarps * p.rpw) << t.tw_log;
+        }
     } else {
         const int n = p.rpw * t.tw;        // values of the warp's rows, 32 or more
         for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += kWarps * p.rpw)
@@ -122,21 +124,70 @@ __device__ __forceinline__ void load_rows(E *tile, const E *src, int64_t L, int6
     }
 }
 
-// The warp's rpw rows at i0 from shared to global memory, values along the lanes.
+// The warp's rows from shared to global memory, values along the lanes.
 template <class E>
-__device__ __forceinline__ void store_rows(const E *tile, E *dst, int64_t L, int64_t left, int i0,
+__device__ __forceinline__ void store_rows(const E *tile, E *dst, int64_t L, int64_t left,
                                            int nrow, const Tiling &t, const Place &p) {
     const int n = p.rpw * t.tw;
-    for (int e = p.lane; e < n; e += 32) {
-        const int i = i0 + (e >> t.tw_log), col = e & (t.tw - 1);
-        if (i < nrow && col < left)
-            dst[i * L + col] = tile[i * t.tw + col];
+    for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += kWarps * p.rpw)
+#pragma unroll 4
+        for (int e = p.lane; e < n; e += 32) {
+            const int i = i0 + (e >> t.tw_log), col = e & (t.tw - 1);
+            if (i < nrow && col < left)
+                dst[i * L + col] = tile[i * t.tw + col];
+        }
+}
+
+// max(|a|, |b|) but for the sign, NaN if either is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+    float r;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// The V codes of a chunk from its values and 1 / step (0: codes 0).  No value is past 127.5
+// steps here: the step follows from the block's largest, and these are far from the end of
+// the fp32 range.
+template <int H>
+__device__ __forceinline__ void code_pairs(const Pair (&v)[H], float inverse, uint32_t (&w)[H / 2]) {
+    const Pair inv = twice(inverse), magic = twice(kCkRound);
+#pragma unroll
+    for (int j = 0; j < H / 2; ++j) {
+        const float2 a = halves(fma2(v[2 * j], inv, magic)), b = halves(fma2(v[2 * j + 1], inv, magic));
+        w[j] = inverse == 0.0f ? 0u : ck_low_bytes(a.x, a.y, b.x, b.y);
     }
 }
 
-template <int V> struct CodeWord;
-template <> struct CodeWord<8> { using type = uint2; };
-template <> struct CodeWord<4> { using type = uint32_t; };
+// V codes as floats.
+template <int H>
+__device__ __forceinline__ void codes_to_pairs(const uint32_t (&w)[H / 2], Pair (&h)[H]) {
+    const Pair bias = twice(-kCkBias);
+#pragma unroll
+    for (int j = 0; j < H / 2; ++j) {
+        const uint32_t f = w[j] ^ 0x80808080u;
+        h[2 * j] = add2(pair(ck_biased(f, 0), ck_biased(f, 1)), bias);
+        h[2 * j + 1] = add2(pair(ck_biased(f, 2), ck_biased(f, 3)), bias);
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void code_words(const int8_t *p, uint32_t (&w)[V / 4]) {
+    if constexpr (V == 8) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        w[0] = u.x;
+        w[1] = u.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void put_code_words(int8_t *p, const uint32_t (&w)[V / 4]) {
+    if constexpr (V == 8)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    else
+        *reinterpret_cast<uint32_t *>(p) = w[0];
+}
 
 // Sums of a group of n values about k.
 struct Moments {
@@ -173,15 +224,16 @@ __device__ __forceinline__ Moments join(At at, Size size) {
 
 template <class T, bool VEC, bool CK>
 __global__ void __launch_bounds__(kThreads) norm_tile_kernel(const NormProblem P, const Tiling t) {
-    constexpr int V = Vec<T>::V;
-    extern __shared__ uint4 tile4[];           // [slice][lpr] chunks
+    constexpr int V = Vec<T>::V, H = Vec<T>::H;
+    extern __shared__ uint4 tile4[];           // [slice][lpr] chunks; !VEC: then codes [slice][tw]
     __shared__ Moments part[kWarps][kMaxTW];   // of a warp's rows, a position
     __shared__ float count[kWarps];
     __shared__ Moments own[kMaxTW];            // of the block's rows (cluster)
     __shared__ float2 stat[kMaxTW];            // (mean, rstd)
     T *tile = reinterpret_cast<T *>(tile4);
+    int8_t *ctile = reinterpret_cast<int8_t *>(tile4 + t.slice * t.lpr);
     const Place p(t);
-    const int rank = blockIdx.x % t.split;
+    const int rank = blockIdx.x % t.split, stride = kWarps * p.rpw;
     const int64_t at = blockIdx.x / t.split;
     const int64_t b = at / t.tiles, l0 = (at - b * t.tiles) * t.tw;
     const int64_t left = P.L - l0;             // positions of this tile (tw or more: all)
@@ -192,55 +244,61 @@ __global__ void __launch_bounds__(kThreads) norm_tile_kernel(const NormProblem P
     copies_landed();
     __syncwarp();
 
-    float f[V], s[V];
+    const uint4 *first = tile4 + p.row * t.lpr + p.sub;
+    const int hop = stride << t.lpr_log;       // chunks between a lane's rows
+    Pair f[H], s[H];
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-        s[j] = 0.0f;
-    float n = 0.0f;
-#pragma unroll 2
-    for (int i = p.row; i < nrow; i += kWarps * p.rpw) {
-        chunk_to_f32<T>(tile4[i * t.lpr + p.sub], f);
-        n += 1.0f;
+    for (int j = 0; j < H; ++j)
+        s[j] = 0;
+    int rows = 0;
+    const uint4 *q = first;
+#pragma unroll 4
+    for (int i = p.row; i < nrow; i += stride, q += hop) {
+        chunk_to_pairs<T>(*q, f);
+        ++rows;
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            s[j] += f[j];
+        for (int j = 0; j < H; ++j)
+            s[j] = add2(s[j], f[j]);
     }
-    for (int o = t.lpr; o < 32; o <<= 1) {
-        n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            s[j] += __shfl_xor_sync(0xFFFFFFFFu, s[j], o);
-    }
-    const float over = n > 0.0f ? 1.0f / n : 0.0f;
-    float mean[V];
-    float s1[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        mean[j] = s[j] * over;
-        s1[j] = s[j] = 0.0f;
-    }
-#pragma unroll 2
-    for (int i = p.row; i < nrow; i += kWarps * p.rpw) {
-        chunk_to_f32<T>(tile4[i * t.lpr + p.sub], f);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float d = f[j] - mean[j];
-            s1[j] += d;
-            s[j] = fmaf(d, d, s[j]);
-        }
-    }
+    auto over_rows = [&](Pair &v) {
+        for (int o = t.lpr; o < 32; o <<= 1)
+            v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    };
     for (int o = t.lpr; o < 32; o <<= 1)
+        rows += __shfl_xor_sync(0xFFFFFFFFu, rows, o);
+    const Pair over = twice(rows > 0 ? -1.0f / (float)rows : 0.0f);
+    Pair neg[H], s1[H];                        // minus the warp's mean
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            s1[j] += __shfl_xor_sync(0xFFFFFFFFu, s1[j], o);
-            s[j] += __shfl_xor_sync(0xFFFFFFFFu, s[j], o);
+    for (int j = 0; j < H; ++j) {
+        over_rows(s[j]);
+        neg[j] = mul2(s[j], over);
+        s1[j] = s[j] = 0;
+    }
+    q = first;
+#pragma unroll 4
+    for (int i = p.row; i < nrow; i += stride, q += hop) {
+        chunk_to_pairs<T>(*q, f);
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            const Pair d = add2(f[j], neg[j]);
+            s1[j] = add2(s1[j], d);
+            s[j] = fma2(d, d, s[j]);
         }
+    }
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+        over_rows(s1[j]);
+        over_rows(s[j]);
+    }
     if (p.lane < t.lpr) {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            part[p.warp][p.sub * V + j] = Moments{mean[j], s1[j], s[j]};
+        for (int j = 0; j < H; ++j) {
+            const float2 k = halves(neg[j]), a = halves(s1[j]), c = halves(s[j]);
+            part[p.warp][p.sub * V + 2 * j] = Moments{-k.x, a.x, c.x};
+            part[p.warp][p.sub * V + 2 * j + 1] = Moments{-k.y, a.y, c.y};
+        }
         if (p.lane == 0)
-            count[p.warp] = n;
+            count[p.warp] = (float)rows;
     }
     __syncthreads();
     const int col = threadIdx.x;
@@ -253,12 +311,12 @@ __global__ void __launch_bounds__(kThreads) norm_tile_kernel(const NormProblem P
         cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();
         if (col < t.tw) {
-            Moments q[kMaxSplit];
+            Moments o[kMaxSplit];
 #pragma unroll
             for (int r = 0; r < kMaxSplit; ++r)
-                q[r] = *cluster.map_shared_rank(&own[col], min(r, t.split - 1));
+                o[r] = *cluster.map_shared_rank(&own[col], min(r, t.split - 1));
             m = join<kMaxSplit>(
-                [&](int r) { return q[r]; },
+                [&](int r) { return o[r]; },
                 [&](int r) {
                     return r < t.split ? (float)max(0, min(t.slice, (int)P.C - r * t.slice)) : 0.0f;
                 });
@@ -277,177 +335,194 @@ __global__ void __launch_bounds__(kThreads) norm_tile_kernel(const NormProblem P
     }
     __syncthreads();
 
-    float rstd[V];
+    Pair rstd[H];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const float2 q = stat[p.sub * V + j];
-        mean[j] = q.x;
-        rstd[j] = q.y;
+    for (int j = 0; j < H; ++j) {
+        const float2 u = stat[p.sub * V + 2 * j], w = stat[p.sub * V + 2 * j + 1];
+        neg[j] = pair(-u.x, -w.x);
+        rstd[j] = pair(u.y, w.y);
     }
+    const bool in = p.sub * V < left;
     const int64_t nb = ck_blocks(P.L);
-    T *y = static_cast<T *>(P.y) + base;
+    const int lanes = min(kCkBlock / V, t.lpr);   // lanes of a block of 32 values
+    const T *gamma = static_cast<const T *>(P.gamma), *beta = static_cast<const T *>(P.beta);
+    uint4 *mine = tile4 + p.row * t.lpr + p.sub;
+    int64_t out = base + p.row * P.L + p.sub * V;
+    int64_t block = (b * P.C + c0 + p.row) * nb + (l0 + p.sub * V) / kCkBlock;
 #pragma unroll 2
-    for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += kWarps * p.rpw) {
+    for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += stride) {
         const int i = i0 + (p.lane >> t.lpr_log);
-        const bool row = i < nrow, in = row && p.sub * V < left;
-        float v[V];
-        chunk_to_f32<T>(tile4[(row ? i : i0) * t.lpr + p.sub], v);
-        const float g = P.gamma && row ? ld_f32(static_cast<const T *>(P.gamma) + c0 + i) : 1.0f;
-        const float be = P.beta && row ? ld_f32(static_cast<const T *>(P.beta) + c0 + i) : 0.0f;
+        const bool row = i < nrow;
+        Pair v[H];
+        chunk_to_pairs<T>(*mine, v);           // rows past nrow: inside the tile, not used
+        const Pair g = twice(gamma && row ? ld_f32(gamma + c0 + i) : 1.0f);
+        const Pair be = twice(beta && row ? ld_f32(beta + c0 + i) : 0.0f);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            v[j] = (v[j] - mean[j]) * rstd[j];
-            f[j] = fmaf(v[j], g, be);
+        for (int j = 0; j < H; ++j) {
+            v[j] = mul2(add2(v[j], neg[j]), rstd[j]);
+            f[j] = fma2(v[j], g, be);
         }
-        if constexpr (VEC) {
-            if (in)
-                *reinterpret_cast<uint4 *>(y + i * P.L + p.sub * V) = f32_to_chunk<T>(f);
-        } else {
+        const uint4 y = pairs_to_chunk<T>(f);
+        if constexpr (!VEC) {
             if (row)
-                tile4[i * t.lpr + p.sub] = f32_to_chunk<T>(f);
-            __syncwarp();
-            store_rows(tile, y, P.L, left, i0, nrow, t, p);
+                *mine = y;
+        } else if (row && in) {
+            *reinterpret_cast<uint4 *>(static_cast<T *>(P.y) + out) = y;
         }
         if constexpr (CK) {
-            uint32_t top = 0;
+            float top = 0.0f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (!row || p.sub * V + j >= left)
-                    v[j] = 0.0f;
-                top = max(top, ck_abs_bits(v[j]));
-            }
-            const int lanes = min(kCkBlock / V, t.lpr);   // lanes of a block of 32 values
-            for (int o = 1; o < lanes; o <<= 1)
-                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            const uint32_t e = ck_scale(top, ck_top<float>());
-            const float inverse = ck_inverse(e);
-            typename CodeWord<V>::type word;
-            int8_t *q = reinterpret_cast<int8_t *>(&word);
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                q[j] = (int8_t)ck_code(v[j], inverse);
-            if constexpr (VEC) {
-                if (in)
-                    *reinterpret_cast<typename CodeWord<V>::type *>(P.codes + base + i * P.L +
-                                                                   p.sub * V) = word;
-            } else {
-                // the rows' bytes over the y that was just stored, one V-byte word a lane
-                __syncwarp();
-                int8_t *rows = reinterpret_cast<int8_t *>(tile + i0 * t.tw);
-                *reinterpret_cast<typename CodeWord<V>::type *>(rows + p.lane * V) = word;
-                __syncwarp();
-                for (int k = p.lane; k < p.rpw * t.tw; k += 32) {
-                    const int ii = i0 + (k >> t.tw_log), col = k & (t.tw - 1);
-                    if (ii < nrow && col < left)
-                        P.codes[base + ii * P.L + col] = rows[k];
+            for (int j = 0; j < H; ++j) {
+                float2 a = halves(v[j]);
+                if constexpr (!VEC) {          // values past the row's end
+                    a.x = p.sub * V + 2 * j < left ? a.x : 0.0f;
+                    a.y = p.sub * V + 2 * j + 1 < left ? a.y : 0.0f;
+                    v[j] = pair(a.x, a.y);
                 }
-                __syncwarp();
+                top = max_abs(max_abs(top, a.x), a.y);
             }
-            if (in && (p.sub & (lanes - 1)) == 0)
-                P.scales[(b * P.C + c0 + i) * nb + (l0 + p.sub * V) / kCkBlock] = (uint8_t)e;
+            uint32_t bits = row && in ? ck_abs_bits(top) : 0u;
+            for (int o = 1; o < lanes; o <<= 1)
+                bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o));
+            const uint32_t e = ck_scale(bits, ck_top<float>());
+            uint32_t w[V / 4];
+            code_pairs<H>(v, ck_inverse(e), w);
+            if constexpr (!VEC)
+                put_code_words<V>(ctile + i * t.tw + p.sub * V, w);
+            else if (row && in)
+                put_code_words<V>(P.codes + out, w);
+            if (row && in && (p.sub & (lanes - 1)) == 0)
+                P.scales[block] = (uint8_t)e;
+            block += stride * nb;
         }
+        mine += hop;
+        out += stride * P.L;
+    }
+    if constexpr (!VEC) {
+        __syncwarp();
+        store_rows(tile, static_cast<T *>(P.y) + base, P.L, left, nrow, t, p);
+        if constexpr (CK)
+            store_rows(ctile, P.codes + base, P.L, left, nrow, t, p);
     }
     if (t.split > 1)
         cg::this_cluster().sync();   // another block may still read this one's `own`
 }
 
+// Shared memory of the gradient's tile kernel for `slice` channels: grad_y and x (or codes,
+// and their steps), each lane's sums of grad_y v and grad_y of its rows, and gamma.
+template <class T>
+__host__ __device__ constexpr int grad_row_bytes(int tw, bool ck) {
+    const int V = 16 / (int)sizeof(T), steps = tw > kCkBlock ? tw / kCkBlock : 1;
+    return tw * (int)sizeof(T) + tw * (ck ? 1 : (int)sizeof(T)) + tw / V * 8 + 4 +
+           (ck ? steps * 4 : 0);
+}
+
 // grad_x tile by tile.  A cluster of t.split blocks walks tiles cluster, cluster + n, ...;
-// each row's sums of grad_y v and grad_y over the walk stay in shared memory with the lane
-// that owns the row, and go to the cluster's rows of `part_g` [clusters][2][C] at the end:
-// a fixed order, no atomics.
+// each lane's sums of grad_y v and grad_y over its rows and the walk stay in shared memory
+// (one addition a row and tile instead of a shuffle tree) and are joined at the end into
+// the cluster's rows of `part_g` [clusters][2][C]: a fixed order, no atomics.
 template <class T, bool VEC, bool CK>
-__global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormGrad P, const Tiling t,
-                                                                  float *part_g) {
-    constexpr int V = Vec<T>::V;
+__global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormGrad P,
+                                                                     const Tiling t,
+                                                                     float *part_g) {
+    constexpr int V = Vec<T>::V, H = Vec<T>::H;
     extern __shared__ uint4 tile4[];           // [slice][lpr] chunks of grad_y, then of x / codes
     __shared__ float2 part[kWarps][kMaxTW];
     __shared__ float2 own[2][kMaxTW];
     __shared__ float2 stat[kMaxTW];            // (A, S)
     T *gtile = reinterpret_cast<T *>(tile4);
-    unsigned char *second = reinterpret_cast<unsigned char *>(tile4 + t.slice * t.lpr);
-    const uint4 *xtile = reinterpret_cast<const uint4 *>(second);
-    int8_t *ctile = reinterpret_cast<int8_t *>(second);
-    float2 *acc = reinterpret_cast<float2 *>(
-        second + (size_t)t.slice * t.tw * (CK ? 1 : sizeof(T)));   // [slice]
+    unsigned char *at_byte = reinterpret_cast<unsigned char *>(tile4 + t.slice * t.lpr);
+    T *xtile = reinterpret_cast<T *>(at_byte);
+    int8_t *ctile = reinterpret_cast<int8_t *>(at_byte);
+    at_byte += (size_t)t.slice * t.tw * (CK ? 1 : sizeof(T));
+    Pair *acc = reinterpret_cast<Pair *>(at_byte);   // [slice][lpr]
+    at_byte += (size_t)t.slice * t.lpr * sizeof(Pair);
+    float *gam = reinterpret_cast<float *>(at_byte);   // [slice]
+    float *steps = gam + t.slice;                      // [slice][spr] (CK)
+    const int spr_log = max(t.tw_log - 5, 0), spr = 1 << spr_log;   // steps of a tile's row
     const Place p(t);
-    const int rank = blockIdx.x % t.split;
+    const int rank = blockIdx.x % t.split, stride = kWarps * p.rpw;
     const int c0 = rank * t.slice;
     const int nrow = min(t.slice, (int)P.C - c0);
     const int64_t nb = ck_blocks(P.L);
-    for (int i = p.row; i < nrow; i += kWarps * p.rpw)
+    const int hop = stride << t.lpr_log;       // chunks between a lane's rows
+    const int first = (p.row << t.lpr_log) + p.sub;
+    for (int i = p.row, k = first; i < nrow; i += stride, k += hop) {
+        acc[k] = 0;
         if (p.sub == 0)
-            acc[i] = make_float2(0.0f, 0.0f);
+            gam[i] = P.gamma ? ld_f32(static_cast<const T *>(P.gamma) + c0 + i) : 1.0f;
+    }
     int turn = 0;
     for (int64_t at = blockIdx.x / t.split; at < t.total; at += gridDim.x / t.split, turn ^= 1) {
         const int64_t b = at / t.tiles, l0 = (at - b * t.tiles) * t.tw;
         const int64_t left = P.L - l0;
         const int64_t base = (b * P.C + c0) * P.L + l0;
+        const bool in = p.sub * V < left;
         load_rows<T, V, VEC>(gtile, static_cast<const T *>(P.gy) + base, P.L, left, nrow, t, p);
-        if constexpr (CK)
+        if constexpr (CK) {
             load_rows<int8_t, V, VEC>(ctile, P.codes + base, P.L, left, nrow, t, p);
-        else
-            load_rows<T, V, VEC>(reinterpret_cast<T *>(second), static_cast<const T *>(P.x) + base,
-                                 P.L, left, nrow, t, p);
-        float rstd[V], mean[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const bool in = p.sub * V + j < left;
-            const int64_t l = b * P.L + l0 + p.sub * V + j;
-            rstd[j] = in ? __ldg(P.rstd + l) : 0.0f;
-            mean[j] = !CK && in ? __ldg(P.mean + l) : 0.0f;
-        }
-        const uint8_t *scale = CK ? P.scales + (b * P.C + c0) * nb + (l0 + p.sub * V) / kCkBlock
-                                  : nullptr;
-        auto values = [&](int i, float (&v)[V]) {
-            if constexpr (CK) {
-                const float step = p.sub * V < left ? ck_step(__ldg(scale + i * nb)) : 0.0f;
-                const typename CodeWord<V>::type word =
-                    *reinterpret_cast<const typename CodeWord<V>::type *>(ctile + i * t.tw +
-                                                                         p.sub * V);
-                const int8_t *q = reinterpret_cast<const int8_t *>(&word);
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    v[j] = (float)q[j] * step;
-            } else {
-                chunk_to_f32<T>(xtile[i * t.lpr + p.sub], v);
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    v[j] = (v[j] - mean[j]) * rstd[j];
+            // the warp's rows' steps, a lane each
+            const int per_log = spr_log + 5 - t.lpr_log;       // log2 of a warp-row group's steps
+            const uint8_t *from = P.scales + (b * P.C + c0) * nb + l0 / kCkBlock;
+            const int k = p.lane & (spr - 1);
+            const bool live = l0 / kCkBlock + k < nb;
+            for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += stride << (5 - per_log)) {
+                const int i = i0 + ((p.lane >> per_log) * stride) +
+                              ((p.lane & ((1 << per_log) - 1)) >> spr_log);
+                if (i < nrow)
+                    steps[(i << spr_log) + k] = live ? ck_step(from[i * nb + k]) : 0.0f;
             }
-        };
+        } else {
+            load_rows<T, V, VEC>(xtile, static_cast<const T *>(P.x) + base, P.L, left, nrow, t, p);
+        }
+        Pair rstd[H], neg[H];                  // neg: minus the mean
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            const int64_t l = b * P.L + l0 + p.sub * V + j;
+            const bool a = p.sub * V + j < left, c = p.sub * V + j + 1 < left;
+            rstd[j / 2] = pair(a ? __ldg(P.rstd + l) : 0.0f, c ? __ldg(P.rstd + l + 1) : 0.0f);
+            neg[j / 2] = 0;
+            if constexpr (!CK)
+                neg[j / 2] = pair(a ? -__ldg(P.mean + l) : 0.0f, c ? -__ldg(P.mean + l + 1) : 0.0f);
+        }
+        const int my_step = (p.sub * V) / kCkBlock;
         copies_landed();
         __syncwarp();
-        float a[V], q[V];
+        // d v = gamma gy v: the checkpoint's v is h step, with one step a chunk, so h is summed
+        // and the step multiplied in once a row
+        Pair a[H], q[H];
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            a[j] = q[j] = 0.0f;
+        for (int j = 0; j < H; ++j)
+            a[j] = q[j] = 0;
 #pragma unroll 2
-        for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += kWarps * p.rpw) {
-            const int i = i0 + (p.lane >> t.lpr_log);
-            const bool row = i < nrow;
-            float g[V], v[V], sg = 0.0f, sb = 0.0f;
-            if (row) {
-                chunk_to_f32<T>(tile4[i * t.lpr + p.sub], g);
-                values(i, v);
-                const float w = P.gamma ? ld_f32(static_cast<const T *>(P.gamma) + c0 + i) : 1.0f;
+        for (int i = p.row, k = first; i < nrow; i += stride, k += hop) {
+            Pair g[H], h[H], sg = 0, sb = 0;
+            chunk_to_pairs<T>(tile4[k], g);
+            const float w = gam[i];
+            float step = 1.0f;
+            if constexpr (CK) {
+                uint32_t words[V / 4];
+                code_words<V>(ctile + k * V, words);
+                codes_to_pairs<H>(words, h);
+                step = steps[(i << spr_log) + my_step];
+            } else {
+                chunk_to_pairs<T>(reinterpret_cast<const uint4 *>(xtile)[k], h);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float d = w * g[j];
-                    a[j] += d;
-                    q[j] = fmaf(d, v[j], q[j]);
-                    sg = fmaf(g[j], v[j], sg);
-                    sb += g[j];
-                }
+                for (int j = 0; j < H; ++j)
+                    h[j] = mul2(add2(h[j], neg[j]), rstd[j]);
+            }
+            const Pair w2 = twice(w), ws = twice(w * step);
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                const Pair gh = mul2(g[j], h[j]);
+                a[j] = fma2(g[j], w2, a[j]);
+                q[j] = fma2(gh, ws, q[j]);
+                sg = add2(sg, gh);
+                sb = add2(sb, g[j]);
             }
             if (part_g) {
-                for (int o = 1; o < t.lpr; o <<= 1) {
-                    sg += __shfl_xor_sync(0xFFFFFFFFu, sg, o);
-                    sb += __shfl_xor_sync(0xFFFFFFFFu, sb, o);
-                }
-                if (row && p.sub == 0) {
-                    acc[i].x += sg;
-                    acc[i].y += sb;
-                }
+                const float2 x = halves(sg), y = halves(sb);
+                acc[k] = add2(acc[k], pair((x.x + x.y) * step, y.x + y.y));
             }
         }
         if (!P.gx) {
@@ -456,14 +531,17 @@ __global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormG
         }
         for (int o = t.lpr; o < 32; o <<= 1)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                a[j] += __shfl_xor_sync(0xFFFFFFFFu, a[j], o);
-                q[j] += __shfl_xor_sync(0xFFFFFFFFu, q[j], o);
+            for (int j = 0; j < H; ++j) {
+                a[j] = add2(a[j], __shfl_xor_sync(0xFFFFFFFFu, a[j], o));
+                q[j] = add2(q[j], __shfl_xor_sync(0xFFFFFFFFu, q[j], o));
             }
         if (p.lane < t.lpr)
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                part[p.warp][p.sub * V + j] = make_float2(a[j], q[j]);
+            for (int j = 0; j < H; ++j) {
+                const float2 x = halves(a[j]), y = halves(q[j]);
+                part[p.warp][p.sub * V + 2 * j] = make_float2(x.x, y.x);
+                part[p.warp][p.sub * V + 2 * j + 1] = make_float2(x.y, y.y);
+            }
         __syncthreads();
         float2 sum = make_float2(0.0f, 0.0f);
         if ((int)threadIdx.x < t.tw) {
@@ -491,46 +569,62 @@ __global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormG
         if ((int)threadIdx.x < t.tw)
             stat[threadIdx.x] = make_float2(sum.x / (float)P.C, sum.y / (float)P.C);
         __syncthreads();
-        float A[V], S[V];
+        // grad_x = rstd gamma gy - rstd A - v rstd S
+        Pair rA[H], rS[H];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float2 o = stat[p.sub * V + j];
-            A[j] = o.x;
-            S[j] = o.y;
+        for (int j = 0; j < H; ++j) {
+            const float2 u = stat[p.sub * V + 2 * j], w = stat[p.sub * V + 2 * j + 1];
+            rA[j] = mul2(pair(-u.x, -w.x), rstd[j]);
+            rS[j] = mul2(pair(-u.y, -w.y), rstd[j]);
         }
-        T *gx = static_cast<T *>(P.gx) + base;
+        T *out = static_cast<T *>(P.gx) + base + p.row * P.L + p.sub * V;
 #pragma unroll 2
-        for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += kWarps * p.rpw) {
-            const int i = i0 + (p.lane >> t.lpr_log);
-            const bool row = i < nrow;
-            if (row) {
-                float g[V], v[V];
-                chunk_to_f32<T>(tile4[i * t.lpr + p.sub], g);
-                values(i, v);
-                const float w = P.gamma ? ld_f32(static_cast<const T *>(P.gamma) + c0 + i) : 1.0f;
+        for (int i = p.row, k = first; i < nrow; i += stride, k += hop, out += stride * P.L) {
+            Pair g[H], h[H];
+            chunk_to_pairs<T>(tile4[k], g);
+            const Pair w2 = twice(gam[i]);
+            if constexpr (CK) {
+                uint32_t words[V / 4];
+                code_words<V>(ctile + k * V, words);
+                codes_to_pairs<H>(words, h);
+                const Pair step = twice(steps[(i << spr_log) + my_step]);
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    g[j] = rstd[j] * (fmaf(w, g[j], -A[j]) - v[j] * S[j]);
-                const uint4 u = f32_to_chunk<T>(g);
-                if constexpr (!VEC)
-                    tile4[i * t.lpr + p.sub] = u;
-                else if (p.sub * V < left)
-                    *reinterpret_cast<uint4 *>(gx + i * P.L + p.sub * V) = u;
+                for (int j = 0; j < H; ++j)
+                    h[j] = mul2(h[j], step);
+            } else {
+                chunk_to_pairs<T>(reinterpret_cast<const uint4 *>(xtile)[k], h);
+#pragma unroll
+                for (int j = 0; j < H; ++j)
+                    h[j] = mul2(add2(h[j], neg[j]), rstd[j]);
             }
-            if constexpr (!VEC) {
-                __syncwarp();
-                store_rows(gtile, gx, P.L, left, i0, nrow, t, p);
-            }
+#pragma unroll
+            for (int j = 0; j < H; ++j)
+                g[j] = fma2(h[j], rS[j], fma2(mul2(g[j], w2), rstd[j], rA[j]));
+            const uint4 u = pairs_to_chunk<T>(g);
+            if constexpr (!VEC)
+                tile4[k] = u;
+            else if (in)
+                *reinterpret_cast<uint4 *>(out) = u;
         }
         __syncwarp();
+        if constexpr (!VEC) {
+            store_rows(gtile, static_cast<T *>(P.gx) + base, P.L, left, nrow, t, p);
+            __syncwarp();
+        }
     }
     if (part_g) {
         float *out = part_g + (int64_t)(blockIdx.x / t.split) * 2 * P.C + c0;
-        for (int i = p.row; i < nrow; i += kWarps * p.rpw)
-            if (p.sub == 0) {
-                out[i] = acc[i].x;
-                out[P.C + i] = acc[i].y;
+        for (int i0 = p.warp * p.rpw, k = first; i0 < nrow; i0 += stride, k += hop) {
+            const int i = i0 + (p.lane >> t.lpr_log);
+            Pair v = i < nrow ? acc[k] : 0;
+            for (int o = 1; o < t.lpr; o <<= 1)
+                v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+            if (i < nrow && p.sub == 0) {
+                const float2 f = halves(v);
+                out[i] = f.x;
+                out[P.C + i] = f.y;
             }
+        }
     }
     if (t.split > 1)
         cg::this_cluster().sync();   // another block may still read this one's `own`
@@ -941,14 +1035,15 @@ int lanes_along(int64_t L) {
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Tiles of [B, C, L] for `bytes` of shared memory a value and `extra` a channel; false when
-// a cluster cannot hold the channels of a tile.
+// Tiles of [B, C, L] for row_bytes(tw) bytes of shared memory a channel; false when a
+// cluster cannot hold the channels of a tile.
 //
 // A block's share is at most a third of an SM's shared memory, so that three blocks are
 // there to load, reduce and store at different times; channels past that are split over a
 // cluster, and so are the channels of a tile where there are too few tiles for the SMs (at
 // least 32 channels a block, four rows a warp).
-bool make_tiling(int64_t B, int64_t C, int64_t L, int size, int bytes, int extra, Tiling *t) {
+template <class Bytes>
+bool make_tiling(int64_t B, int64_t C, int64_t L, int size, Bytes row_bytes, Tiling *t) {
     const int V = 16 / size;
     if (L < 2)
         return false;
@@ -962,7 +1057,7 @@ bool make_tiling(int64_t B, int64_t C, int64_t L, int size, int bytes, int extra
     t->tiles = (L + t->tw - 1) / t->tw;
     t->total = B * t->tiles;
     auto slice = [&](int split) { return ((C + split - 1) / split + rpw - 1) / rpw * rpw; };
-    auto shared = [&](int split) { return slice(split) * (t->tw * bytes + extra); };
+    auto shared = [&](int split) { return slice(split) * row_bytes(t->tw); };
     t->split = 1;
     while (t->split < kMaxSplit && shared(t->split) > 70 * 1024)
         t->split *= 2;
@@ -978,7 +1073,7 @@ bool make_tiling(int64_t B, int64_t C, int64_t L, int size, int bytes, int extra
 // Blocks of a tile kernel that one SM holds.
 int blocks_per_sm(size_t shared) {
     const int n = (int)((227 * 1024) / (shared + 8 * 1024));   // 8 KB: static and reserved
-    return n < 1 ? 1 : n > 6 ? 6 : n;
+    return n < 1 ? 1 : n > 3 ? 3 : n;   // 3: registers
 }
 
 template <class... A>
@@ -1031,10 +1126,11 @@ cudaError_t norm(const NormProblem &P, cudaStream_t s) {
             return cudaGetLastError();
     }
     Tiling t;
-    if (make_tiling(P.B, P.C, P.L, sizeof(T), sizeof(T), 0, &t)) {
+    const bool vec = base && P.L % V == 0;
+    auto row_bytes = [&](int tw) { return tw * (int)sizeof(T) + (!vec && P.codes ? tw : 0); };
+    if (make_tiling(P.B, P.C, P.L, sizeof(T), row_bytes, &t)) {
         const unsigned grid = (unsigned)(t.total * t.split);
-        const size_t shared = (size_t)t.slice * t.tw * sizeof(T);
-        const bool vec = base && P.L % V == 0;
+        const size_t shared = (size_t)t.slice * row_bytes(t.tw);
         auto kernel = vec ? (P.codes ? norm_tile_kernel<T, true, true> : norm_tile_kernel<T, true, false>)
                           : (P.codes ? norm_tile_kernel<T, false, true> : norm_tile_kernel<T, false, false>);
         return launch_cluster(kernel, grid, (unsigned)t.split, shared, s, P, t);
@@ -1074,11 +1170,11 @@ GradPlan grad_plan(const NormGrad &P) {
             return g;
         }
     }
-    const int second = P.from_codes ? 1 : (int)sizeof(T);
-    if (make_tiling(P.B, P.C, P.L, sizeof(T), (int)sizeof(T) + second, sizeof(float2), &g.t)) {
+    auto row_bytes = [&](int tw) { return grad_row_bytes<T>(tw, P.from_codes); };
+    if (make_tiling(P.B, P.C, P.L, sizeof(T), row_bytes, &g.t)) {
         g.kind = 1;
         g.vec = base && P.L % V == 0;
-        g.shared = (size_t)g.t.slice * (g.t.tw * (sizeof(T) + second) + sizeof(float2));
+        g.shared = (size_t)g.t.slice * row_bytes(g.t.tw);
         const int64_t room = (int64_t)sms * blocks_per_sm(g.shared) / g.t.split;
         g.rows = g.t.total < room ? g.t.total : room;
         g.blocks = g.rows * g.t.split;
@@ -1132,9 +1228,16 @@ cudaError_t norm_grad(const NormGrad &P, void *ws, cudaStream_t s, int *launches
     return cudaGetLastError();
 }
 
+// For any alignment of the tensors, so that a caller can keep the size of a shape.
 template <class T>
-size_t grad_workspace(const NormGrad &P) {
-    return (size_t)grad_plan<T>(P).rows * 2 * P.C * sizeof(float);
+size_t grad_workspace(NormGrad P) {
+    P.gamma = nullptr;
+    P.x = P.gy = P.codes = nullptr;   // aligned
+    P.gx = nullptr;
+    const int64_t a = grad_plan<T>(P).rows;
+    P.gy = reinterpret_cast<const void *>((uintptr_t)1);
+    const int64_t b = grad_plan<T>(P).rows;
+    return (size_t)(a > b ? a : b) * 2 * P.C * sizeof(float);
 }
 
 }  // namespace
