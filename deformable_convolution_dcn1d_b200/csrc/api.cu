@@ -473,6 +473,7 @@ struct CheckpointBackward {
     Problem P;
     BackwardGrads G;
     size_t x_bytes, total;
+    bool depthwise;   // one kernel that reads the checkpoint itself
 };
 
 int validate_checkpoint_backward(
@@ -503,8 +504,10 @@ int validate_checkpoint_backward(
             return st;
     R->ck = CkProblem{B, C, L, x.dtype, nullptr, data_of<void>(gamma), data_of<void>(beta),
                       codes->data, scales->data, nullptr};
-    R->x_bytes = round256((size_t)(B * C * L) * (x.dtype == DCN1D_F32 ? 4 : 2));
-    R->total = R->x_bytes + backward_workspace(R->P, R->G);
+    R->depthwise = depthwise_grad_supported(R->P);
+    R->x_bytes = R->depthwise ? 0 : round256((size_t)(B * C * L) * (x.dtype == DCN1D_F32 ? 4 : 2));
+    R->total = R->depthwise ? depthwise_grad_workspace(R->P, R->G)
+                            : R->x_bytes + backward_workspace(R->P, R->G);
     return DCN1D_OK;
 }
 
@@ -1131,6 +1134,14 @@ int dcn1d_backward_checkpoint(
         return DCN1D_ERR_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int launches = 0, unpacked = 0;
+    if (R.depthwise) {
+        const CheckpointConv q{R.P, R.G, static_cast<const int8_t *>(R.ck.codes),
+                               static_cast<const uint8_t *>(R.ck.scales), R.ck.gamma, R.ck.beta};
+        if (launch_depthwise_grad(q, workspace, s, &launches) != cudaSuccess)
+            return DCN1D_ERR_LAUNCH;
+        g_last_launches = launches;
+        return DCN1D_OK;
+    }
     if (R.ck.B > 0) {
         R.P.x = R.ck.out = workspace;
         if (launch_checkpoint_unpack(R.ck, s) != cudaSuccess)

@@ -166,6 +166,19 @@ struct CkProblem {
 };
 cudaError_t launch_checkpoint_pack(const CkProblem &P, cudaStream_t stream);
 cudaError_t launch_checkpoint_unpack(const CkProblem &P, cudaStream_t stream);
+// A backward whose input is a checkpoint of [B, C_in, L_in], and its one-kernel form for the
+// depthwise layer with offsets of each channel's own (depthwise_grad.cu).  P.x is not used.
+struct CheckpointConv {
+    Problem P;
+    BackwardGrads G;
+    const int8_t *codes;
+    const uint8_t *scales;
+    const void *gamma, *beta;
+};
+bool depthwise_grad_supported(const Problem &P);
+size_t depthwise_grad_workspace(const Problem &P, const BackwardGrads &G);
+cudaError_t launch_depthwise_grad(const CheckpointConv &q, void *workspace, cudaStream_t stream,
+                                  int *launches);
 // SM count of the current device, or `other` where it cannot be read (no device).
 int sm_count_or(int other);
 cudaError_t launch_sample_index(const void *off, int dtype, int B, int G, int L_out, int K,
