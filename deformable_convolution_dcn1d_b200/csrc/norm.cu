@@ -30,7 +30,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kRowBytes = 128;                 // a tile's share of one channel's row, at most
 constexpr int kMaxTW = kRowBytes / 2;
 constexpr int kMaxSplit = 8;                   // blocks of a portable cluster
@@ -38,9 +38,11 @@ constexpr int kMaxSplit = 8;                   // blocks of a portable cluster
 // How a launch cuts [B, C, L] into tiles.
 struct Tiling {
     int tw, tw_log;    // positions of a tile, a power of two
-    int lpr, lpr_log;  // lanes of a row: tw / V
+    int lpr_log;       // log2 of the lanes of a row: tw / V
     int split;         // blocks that share the channels of a tile (a cluster)
-    int slice;         // channels of a block, a multiple of a warp's rows
+    int slice;         // channels of a block, a multiple of the rows of its threads
+    int walk_b, walk_l;   // a walk's step over (b, tile of b): the number of clusters
+    float inv_c;       // 1 / C
     int64_t tiles;     // tiles of one b
     int64_t total;     // tiles in all
 };
@@ -82,60 +84,81 @@ __device__ __forceinline__ void copies_landed() {
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Where a thread stands in its block's tile.
+// Where a thread stands in its block's tile.  Chunk k of a tile is row k / lpr, part k % lpr;
+// a thread owns chunks threadIdx.x + j kThreads, j < n, so all its shared addresses are
+// constants apart.  LPR_LOG < 0: from the tiling.
+template <int LPR_LOG>
 struct Place {
-    int warp, lane, sub, rpw, row;   // rpw: rows of a warp; row: this lane's first row
-    __device__ Place(const Tiling &t) {
-        warp = threadIdx.x / 32;
+    int lpr_log, lane, sub, row, stride, n, warp_n;   // warp_n: the largest n of the warp
+    __device__ Place(const Tiling &t, int nrow) {
+        lpr_log = LPR_LOG >= 0 ? LPR_LOG : t.lpr_log;
         lane = threadIdx.x & 31;
-        sub = lane & (t.lpr - 1);
-        rpw = 32 >> t.lpr_log;
-        row = warp * rpw + (lane >> t.lpr_log);
+        sub = lane & ((1 << lpr_log) - 1);
+        row = (int)threadIdx.x >> lpr_log;
+        stride = kThreads >> lpr_log;
+        const int shift = __ffs(stride) - 1;
+        n = max(0, (nrow - row + stride - 1) >> shift);
+        warp_n = max(0, (nrow - ((int)(threadIdx.x & ~31u) >> lpr_log) + stride - 1) >> shift);
     }
 };
 
-// The warp's rows of a block's slice, `E` values (T, or codes): global rows start at
-// src + row * L, shared rows are tw values.  VEC: each lane copies its own chunk (rows are
-// aligned for it and hold whole chunks).  Otherwise lanes run along the values, and the
-// warp meets afterwards.
-template <class E, int V, bool VEC>
+// A block's rows of `E` values (T, or codes), tw a row: global rows start at src + row * L.
+// VEC: each thread copies its own chunks (rows are aligned for it and hold whole chunks).
+// Otherwise lanes run along the values, each warp over the rows of its threads' chunks, and
+// the warp meets afterwards; 4-byte values are copied asynchronously too.
+template <class E, int V, bool VEC, class P>
 __device__ __forceinline__ void load_rows(E *tile, const E *src, int64_t L, int64_t left, int nrow,
-                                          const Tiling &t, const Place &p) {
+                                          const Tiling &t, const P &p) {
     if constexpr (VEC) {
         const bool in = p.sub * V < left;
         const E *from = in ? src + p.row * L + p.sub * V : src;
-        const int64_t step = in ? (int64_t)kWarps * p.rpw * L : 0;
-        E *to = tile + p.row * t.tw + p.sub * V;
+        const int64_t step = in ? p.stride * L : 0;
+        E *to = tile + threadIdx.x * V;
 #pragma unroll 4
-        for (int i = p.row; i < nrow; i += kWarps * p.rpw) {
-            copy_async<V * (int)sizeof(E)>(to, from, in);
+        for (int j = 0; j < p.n; ++j) {
+            copy_async<V * (int)sizeof(E)>(to + j * kThreads * V, from, in);
             from += step;
-            to += (kWarps * p.rpw) << t.tw_log;
         }
     } else {
-        const int n = p.rpw * t.tw;        // values of the warp's rows, 32 or more
-        for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += kWarps * p.rpw)
-#pragma unroll 4
-            for (int e = p.lane; e < n; e += 32) {
-                const int i = i0 + (e >> t.tw_log), col = e & (t.tw - 1);
-                if (i < nrow)
-                    tile[i * t.tw + col] = col < left ? src[i * L + col] : E(0.0f);
+        const int row0 = (int)(threadIdx.x & ~31u) >> p.lpr_log;   // the warp's first row
+#pragma unroll 2
+        for (int j = 0; j < p.warp_n; ++j) {
+            E *to = tile + ((threadIdx.x & ~31u) + j * kThreads) * V;
+            const E *from = src + (row0 + j * p.stride) * L;
+            E v[V];
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+                const int e = p.lane + 32 * q, r = e >> t.tw_log, col = e & (t.tw - 1);
+                const bool in = row0 + j * p.stride + r < nrow && col < left;
+                if constexpr (sizeof(E) == 4)
+                    copy_async<4>(to + e, in ? from + r * L + col : src, in);
+                else
+                    v[q] = in ? from[r * L + col] : E(0.0f);
             }
+            if constexpr (sizeof(E) < 4)
+#pragma unroll
+                for (int q = 0; q < V; ++q)
+                    to[p.lane + 32 * q] = v[q];
+        }
     }
 }
 
-// The warp's rows from shared to global memory, values along the lanes.
-template <class E>
-__device__ __forceinline__ void store_rows(const E *tile, E *dst, int64_t L, int64_t left,
-                                           int nrow, const Tiling &t, const Place &p) {
-    const int n = p.rpw * t.tw;
-    for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += kWarps * p.rpw)
-#pragma unroll 4
-        for (int e = p.lane; e < n; e += 32) {
-            const int i = i0 + (e >> t.tw_log), col = e & (t.tw - 1);
-            if (i < nrow && col < left)
-                dst[i * L + col] = tile[i * t.tw + col];
+// The same rows back to global memory, values along the lanes.
+template <class E, int V, class P>
+__device__ __forceinline__ void store_rows(const E *tile, E *dst, int64_t L, int64_t left, int nrow,
+                                           const Tiling &t, const P &p) {
+    const int row0 = (int)(threadIdx.x & ~31u) >> p.lpr_log;
+#pragma unroll 2
+    for (int j = 0; j < p.warp_n; ++j) {
+        const E *from = tile + ((threadIdx.x & ~31u) + j * kThreads) * V;
+        E *to = dst + (row0 + j * p.stride) * L;
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+            const int e = p.lane + 32 * q, r = e >> t.tw_log, col = e & (t.tw - 1);
+            if (row0 + j * p.stride + r < nrow && col < left)
+                to[r * L + col] = from[e];
         }
+    }
 }
 
 // max(|a|, |b|) but for the sign, NaN if either is.
@@ -222,62 +245,65 @@ __device__ __forceinline__ Moments join(At at, Size size) {
     return r;
 }
 
-template <class T, bool VEC, bool CK>
+template <class T, bool VEC, bool CK, int LPR_LOG>
 __global__ void __launch_bounds__(kThreads) norm_tile_kernel(const NormProblem P, const Tiling t) {
     constexpr int V = Vec<T>::V, H = Vec<T>::H;
-    extern __shared__ uint4 tile4[];           // [slice][lpr] chunks; !VEC: then codes [slice][tw]
+    extern __shared__ uint4 tile4[];           // chunks of the slice; !VEC: then its codes
     __shared__ Moments part[kWarps][kMaxTW];   // of a warp's rows, a position
     __shared__ float count[kWarps];
     __shared__ Moments own[kMaxTW];            // of the block's rows (cluster)
-    __shared__ float2 stat[kMaxTW];            // (mean, rstd)
+    __shared__ float2 stat[kMaxTW];            // (-mean, rstd)
     T *tile = reinterpret_cast<T *>(tile4);
-    int8_t *ctile = reinterpret_cast<int8_t *>(tile4 + t.slice * t.lpr);
-    const Place p(t);
-    const int rank = blockIdx.x % t.split, stride = kWarps * p.rpw;
-    const int64_t at = blockIdx.x / t.split;
-    const int64_t b = at / t.tiles, l0 = (at - b * t.tiles) * t.tw;
+    const int rank = t.split > 1 ? blockIdx.x % t.split : 0;
+    const unsigned at = t.split > 1 ? blockIdx.x / t.split : blockIdx.x;
+    const unsigned tiles = (unsigned)t.tiles, bu = at / tiles;
+    const int64_t b = bu, l0 = (int64_t)(at - bu * tiles) << t.tw_log;
     const int64_t left = P.L - l0;             // positions of this tile (tw or more: all)
     const int c0 = rank * t.slice;
     const int nrow = min(t.slice, (int)P.C - c0);   // may be 0 or less in the last blocks
+    const Place<LPR_LOG> p(t, nrow);
+    int8_t *ctile = reinterpret_cast<int8_t *>(tile4 + (t.slice << p.lpr_log));
     const int64_t base = (b * P.C + c0) * P.L + l0;
     load_rows<T, V, VEC>(tile, static_cast<const T *>(P.x) + base, P.L, left, nrow, t, p);
     copies_landed();
     __syncwarp();
 
-    const uint4 *first = tile4 + p.row * t.lpr + p.sub;
-    const int hop = stride << t.lpr_log;       // chunks between a lane's rows
+    uint4 *mine = tile4 + threadIdx.x;
     Pair f[H], s[H];
 #pragma unroll
     for (int j = 0; j < H; ++j)
         s[j] = 0;
-    int rows = 0;
-    const uint4 *q = first;
 #pragma unroll 4
-    for (int i = p.row; i < nrow; i += stride, q += hop) {
-        chunk_to_pairs<T>(*q, f);
-        ++rows;
+    for (int k = 0; k < p.n; ++k) {
+        chunk_to_pairs<T>(mine[k * kThreads], f);
 #pragma unroll
         for (int j = 0; j < H; ++j)
             s[j] = add2(s[j], f[j]);
     }
-    auto over_rows = [&](Pair &v) {
-        for (int o = t.lpr; o < 32; o <<= 1)
-            v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    auto over_rows = [&](Pair &v) {            // the lanes that hold the same positions
+        if constexpr (LPR_LOG >= 0) {
+#pragma unroll
+            for (int o = 1 << LPR_LOG; o < 32; o <<= 1)
+                v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+        } else {
+            for (int o = 1 << p.lpr_log; o < 32; o <<= 1)
+                v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+        }
     };
-    for (int o = t.lpr; o < 32; o <<= 1)
+    int rows = p.n;
+    for (int o = 1 << p.lpr_log; o < 32; o <<= 1)
         rows += __shfl_xor_sync(0xFFFFFFFFu, rows, o);
     const Pair over = twice(rows > 0 ? -1.0f / (float)rows : 0.0f);
-    Pair neg[H], s1[H];                        // minus the warp's mean
+    Pair neg[H], s1[H];                        // neg: minus the warp's mean
 #pragma unroll
     for (int j = 0; j < H; ++j) {
         over_rows(s[j]);
         neg[j] = mul2(s[j], over);
         s1[j] = s[j] = 0;
     }
-    q = first;
 #pragma unroll 4
-    for (int i = p.row; i < nrow; i += stride, q += hop) {
-        chunk_to_pairs<T>(*q, f);
+    for (int k = 0; k < p.n; ++k) {
+        chunk_to_pairs<T>(mine[k * kThreads], f);
 #pragma unroll
         for (int j = 0; j < H; ++j) {
             const Pair d = add2(f[j], neg[j]);
@@ -290,15 +316,15 @@ __global__ void __launch_bounds__(kThreads) norm_tile_kernel(const NormProblem P
         over_rows(s1[j]);
         over_rows(s[j]);
     }
-    if (p.lane < t.lpr) {
+    if (p.lane < (1 << p.lpr_log)) {
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-            const float2 k = halves(neg[j]), a = halves(s1[j]), c = halves(s[j]);
-            part[p.warp][p.sub * V + 2 * j] = Moments{-k.x, a.x, c.x};
-            part[p.warp][p.sub * V + 2 * j + 1] = Moments{-k.y, a.y, c.y};
+            const float2 k = halves(neg[j]), u = halves(s1[j]), w = halves(s[j]);
+            part[threadIdx.x / 32][p.sub * V + 2 * j] = Moments{-k.x, u.x, w.x};
+            part[threadIdx.x / 32][p.sub * V + 2 * j + 1] = Moments{-k.y, u.y, w.y};
         }
         if (p.lane == 0)
-            count[p.warp] = (float)rows;
+            count[threadIdx.x / 32] = (float)rows;
     }
     __syncthreads();
     const int col = threadIdx.x;
@@ -323,9 +349,9 @@ __global__ void __launch_bounds__(kThreads) norm_tile_kernel(const NormProblem P
         }
     }
     if (col < t.tw) {
-        const float off = m.s1 / (float)P.C, var = fmaxf(m.s2 / (float)P.C - off * off, 0.0f);
+        const float off = m.s1 * t.inv_c, var = fmaxf(m.s2 * t.inv_c - off * off, 0.0f);
         const float rstd = 1.0f / sqrtf((m.s2 == m.s2 ? var : m.s2) + P.eps);   // fmaxf drops NaN
-        stat[col] = make_float2(m.k + off, rstd);
+        stat[col] = make_float2(-(m.k + off), rstd);
         if (rank == 0 && col < left) {
             if (P.mean)
                 P.mean[b * P.L + l0 + col] = m.k + off;
@@ -339,35 +365,40 @@ __global__ void __launch_bounds__(kThreads) norm_tile_kernel(const NormProblem P
 #pragma unroll
     for (int j = 0; j < H; ++j) {
         const float2 u = stat[p.sub * V + 2 * j], w = stat[p.sub * V + 2 * j + 1];
-        neg[j] = pair(-u.x, -w.x);
+        neg[j] = pair(u.x, w.x);
         rstd[j] = pair(u.y, w.y);
     }
     const bool in = p.sub * V < left;
     const int64_t nb = ck_blocks(P.L);
-    const int lanes = min(kCkBlock / V, t.lpr);   // lanes of a block of 32 values
-    const T *gamma = static_cast<const T *>(P.gamma), *beta = static_cast<const T *>(P.beta);
-    uint4 *mine = tile4 + p.row * t.lpr + p.sub;
-    int64_t out = base + p.row * P.L + p.sub * V;
-    int64_t block = (b * P.C + c0 + p.row) * nb + (l0 + p.sub * V) / kCkBlock;
+    const int lanes = min(kCkBlock / V, 1 << p.lpr_log);   // lanes of a block of 32 values
+    const T *gamma = P.gamma ? static_cast<const T *>(P.gamma) + c0 + p.row : nullptr;
+    const T *beta = P.beta ? static_cast<const T *>(P.beta) + c0 + p.row : nullptr;
+    T *y = static_cast<T *>(P.y) + base + p.row * P.L + p.sub * V;
+    int8_t *codes = P.codes + base + p.row * P.L + p.sub * V;
+    uint8_t *scale = P.scales + (b * P.C + c0 + p.row) * nb + (l0 + p.sub * V) / kCkBlock;
+    const int64_t hop = p.stride * P.L, scale_hop = p.stride * nb;
+    // CK: whole warps walk together, for the block maximum's shuffles
+    const int n = CK ? p.warp_n : p.n;
 #pragma unroll 2
-    for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += stride) {
-        const int i = i0 + (p.lane >> t.lpr_log);
-        const bool row = i < nrow;
+    for (int k = 0; k < n; ++k) {
+        const bool row = !CK || k < p.n;
         Pair v[H];
-        chunk_to_pairs<T>(*mine, v);           // rows past nrow: inside the tile, not used
-        const Pair g = twice(gamma && row ? ld_f32(gamma + c0 + i) : 1.0f);
-        const Pair be = twice(beta && row ? ld_f32(beta + c0 + i) : 0.0f);
+        chunk_to_pairs<T>(mine[k * kThreads], v);   // rows past nrow: inside the tile, not used
+        const Pair g = twice(gamma && row ? ld_f32(gamma + k * p.stride) : 1.0f);
+        const Pair be = twice(beta && row ? ld_f32(beta + k * p.stride) : 0.0f);
 #pragma unroll
         for (int j = 0; j < H; ++j) {
             v[j] = mul2(add2(v[j], neg[j]), rstd[j]);
             f[j] = fma2(v[j], g, be);
         }
-        const uint4 y = pairs_to_chunk<T>(f);
+        const uint4 o = pairs_to_chunk<T>(f);
         if constexpr (!VEC) {
             if (row)
-                *mine = y;
-        } else if (row && in) {
-            *reinterpret_cast<uint4 *>(static_cast<T *>(P.y) + out) = y;
+                mine[k * kThreads] = o;
+        } else {
+            if (row && in)
+                *reinterpret_cast<uint4 *>(y) = o;
+            y += hop;
         }
         if constexpr (CK) {
             float top = 0.0f;
@@ -382,244 +413,290 @@ __global__ void __launch_bounds__(kThreads) norm_tile_kernel(const NormProblem P
                 top = max_abs(max_abs(top, a.x), a.y);
             }
             uint32_t bits = row && in ? ck_abs_bits(top) : 0u;
-            for (int o = 1; o < lanes; o <<= 1)
-                bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o));
+            if constexpr (LPR_LOG >= 0) {
+#pragma unroll
+                for (int o2 = 1; o2 < kCkBlock / V && o2 < (1 << LPR_LOG); o2 <<= 1)
+                    bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o2));
+            } else {
+                for (int o2 = 1; o2 < lanes; o2 <<= 1)
+                    bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o2));
+            }
             const uint32_t e = ck_scale(bits, ck_top<float>());
             uint32_t w[V / 4];
             code_pairs<H>(v, ck_inverse(e), w);
             if constexpr (!VEC)
-                put_code_words<V>(ctile + i * t.tw + p.sub * V, w);
+                put_code_words<V>(ctile + (threadIdx.x + k * kThreads) * V, w);
             else if (row && in)
-                put_code_words<V>(P.codes + out, w);
+                put_code_words<V>(codes, w);
             if (row && in && (p.sub & (lanes - 1)) == 0)
-                P.scales[block] = (uint8_t)e;
-            block += stride * nb;
+                *scale = (uint8_t)e;
+            codes += hop;
+            scale += scale_hop;
         }
-        mine += hop;
-        out += stride * P.L;
     }
     if constexpr (!VEC) {
         __syncwarp();
-        store_rows(tile, static_cast<T *>(P.y) + base, P.L, left, nrow, t, p);
+        store_rows<T, V>(tile, static_cast<T *>(P.y) + base, P.L, left, nrow, t, p);
         if constexpr (CK)
-            store_rows(ctile, P.codes + base, P.L, left, nrow, t, p);
+            store_rows<int8_t, V>(ctile, P.codes + base, P.L, left, nrow, t, p);
     }
     if (t.split > 1)
         cg::this_cluster().sync();   // another block may still read this one's `own`
 }
 
-// Shared memory of the gradient's tile kernel for `slice` channels: grad_y and x (or codes,
-// and their steps), each lane's sums of grad_y v and grad_y of its rows, and gamma.
+// Shared memory of the gradient's tile kernel for a channel: grad_y and x (or codes), each
+// lane's sums of grad_y v and grad_y of its rows, and gamma with the steps of the codes.
 template <class T>
-__host__ __device__ constexpr int grad_row_bytes(int tw, bool ck) {
-    const int V = 16 / (int)sizeof(T), steps = tw > kCkBlock ? tw / kCkBlock : 1;
-    return tw * (int)sizeof(T) + tw * (ck ? 1 : (int)sizeof(T)) + tw / V * 8 + 4 +
-           (ck ? steps * 4 : 0);
+constexpr int grad_row_bytes(int tw, bool ck) {
+    const int V = 16 / (int)sizeof(T), steps = ck && tw > kCkBlock ? tw / kCkBlock : 1;
+    return tw * (int)sizeof(T) + tw * (ck ? 1 : (int)sizeof(T)) + tw / V * 8 + steps * 8;
 }
 
 // grad_x tile by tile.  A cluster of t.split blocks walks tiles cluster, cluster + n, ...;
 // each lane's sums of grad_y v and grad_y over its rows and the walk stay in shared memory
 // (one addition a row and tile instead of a shuffle tree) and are joined at the end into
 // the cluster's rows of `part_g` [clusters][2][C]: a fixed order, no atomics.
-template <class T, bool VEC, bool CK>
-__global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormGrad P,
+template <class T, bool VEC, bool CK, int LPR_LOG>
+__global__ void __launch_bounds__(kThreads, 5) norm_grad_tile_kernel(const NormGrad P,
                                                                      const Tiling t,
                                                                      float *part_g) {
     constexpr int V = Vec<T>::V, H = Vec<T>::H;
-    extern __shared__ uint4 tile4[];           // [slice][lpr] chunks of grad_y, then of x / codes
+    extern __shared__ uint4 tile4[];           // chunks of grad_y, then of x / codes
     __shared__ float2 part[kWarps][kMaxTW];
     __shared__ float2 own[2][kMaxTW];
-    __shared__ float2 stat[kMaxTW];            // (A, S)
-    T *gtile = reinterpret_cast<T *>(tile4);
-    unsigned char *at_byte = reinterpret_cast<unsigned char *>(tile4 + t.slice * t.lpr);
-    T *xtile = reinterpret_cast<T *>(at_byte);
-    int8_t *ctile = reinterpret_cast<int8_t *>(at_byte);
-    at_byte += (size_t)t.slice * t.tw * (CK ? 1 : sizeof(T));
-    Pair *acc = reinterpret_cast<Pair *>(at_byte);   // [slice][lpr]
-    at_byte += (size_t)t.slice * t.lpr * sizeof(Pair);
-    float *gam = reinterpret_cast<float *>(at_byte);   // [slice]
-    float *steps = gam + t.slice;                      // [slice][spr] (CK)
-    const int spr_log = max(t.tw_log - 5, 0), spr = 1 << spr_log;   // steps of a tile's row
-    const Place p(t);
-    const int rank = blockIdx.x % t.split, stride = kWarps * p.rpw;
+    __shared__ float2 stat[kMaxTW];            // (-A, -S)
+    const int rank = t.split > 1 ? blockIdx.x % t.split : 0;
+    const unsigned cluster_at = t.split > 1 ? blockIdx.x / t.split : blockIdx.x;
     const int c0 = rank * t.slice;
     const int nrow = min(t.slice, (int)P.C - c0);
+    const Place<LPR_LOG> p(t, nrow);
+    T *gtile = reinterpret_cast<T *>(tile4);
+    unsigned char *at_byte = reinterpret_cast<unsigned char *>(tile4 + (t.slice << p.lpr_log));
+    T *xtile = reinterpret_cast<T *>(at_byte);
+    int8_t *ctile = reinterpret_cast<int8_t *>(at_byte);
+    at_byte += ((size_t)t.slice << t.tw_log) * (CK ? 1 : sizeof(T));
+    Pair *acc = reinterpret_cast<Pair *>(at_byte);         // a chunk
+    at_byte += ((size_t)t.slice << p.lpr_log) * sizeof(Pair);
+    float2 *scaled = reinterpret_cast<float2 *>(at_byte);  // [slice][spr]: gamma, step
+    const int spr_log = CK ? max(t.tw_log - 5, 0) : 0, spr = 1 << spr_log;   // steps of a row
     const int64_t nb = ck_blocks(P.L);
-    const int hop = stride << t.lpr_log;       // chunks between a lane's rows
-    const int first = (p.row << t.lpr_log) + p.sub;
-    for (int i = p.row, k = first; i < nrow; i += stride, k += hop) {
-        acc[k] = 0;
-        if (p.sub == 0)
-            gam[i] = P.gamma ? ld_f32(static_cast<const T *>(P.gamma) + c0 + i) : 1.0f;
+    const T *gamma = P.gamma ? static_cast<const T *>(P.gamma) + c0 : nullptr;
+    for (int k = 0; k < p.n; ++k) {
+        acc[threadIdx.x + k * kThreads] = 0;
+        const int i = p.row + k * p.stride;
+        if (!CK && p.sub == 0)
+            scaled[i] = make_float2(gamma ? ld_f32(gamma + i) : 1.0f, 1.0f);
     }
+    const uint4 *gmine = tile4 + threadIdx.x;
+    const int8_t *cmine = ctile + threadIdx.x * V;
+    const uint4 *xmine = reinterpret_cast<const uint4 *>(xtile) + threadIdx.x;
+    const float2 *smine = scaled + (p.row << spr_log) + (CK ? (p.sub * V) / kCkBlock : 0);
+    const int shop = p.stride << spr_log;
+    auto over_rows = [&](Pair &v) {            // the lanes that hold the same positions
+        if constexpr (LPR_LOG >= 0) {
+#pragma unroll
+            for (int o = 1 << LPR_LOG; o < 32; o <<= 1)
+                v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+        } else {
+            for (int o = 1 << p.lpr_log; o < 32; o <<= 1)
+                v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+        }
+    };
     int turn = 0;
-    for (int64_t at = blockIdx.x / t.split; at < t.total; at += gridDim.x / t.split, turn ^= 1) {
-        const int64_t b = at / t.tiles, l0 = (at - b * t.tiles) * t.tw;
+    const unsigned tiles = (unsigned)t.tiles;
+    int64_t b = cluster_at / tiles;
+    unsigned lt = cluster_at - (unsigned)b * tiles;
+    while (b < P.B) {
+        const int64_t l0 = (int64_t)lt << t.tw_log;
         const int64_t left = P.L - l0;
         const int64_t base = (b * P.C + c0) * P.L + l0;
         const bool in = p.sub * V < left;
         load_rows<T, V, VEC>(gtile, static_cast<const T *>(P.gy) + base, P.L, left, nrow, t, p);
         if constexpr (CK) {
             load_rows<int8_t, V, VEC>(ctile, P.codes + base, P.L, left, nrow, t, p);
-            // the warp's rows' steps, a lane each
-            const int per_log = spr_log + 5 - t.lpr_log;       // log2 of a warp-row group's steps
+            // gamma and the steps of the warp's rows, one of each a lane
+            const int per_log = spr_log + 5 - p.lpr_log;   // log2 of the steps of a warp's rows
             const uint8_t *from = P.scales + (b * P.C + c0) * nb + l0 / kCkBlock;
             const int k = p.lane & (spr - 1);
             const bool live = l0 / kCkBlock + k < nb;
-            for (int i0 = p.warp * p.rpw; i0 < nrow; i0 += stride << (5 - per_log)) {
-                const int i = i0 + ((p.lane >> per_log) * stride) +
+            const int first = ((int)(threadIdx.x & ~31u) >> p.lpr_log) +
+                              (p.lane >> per_log) * p.stride +
                               ((p.lane & ((1 << per_log) - 1)) >> spr_log);
-                if (i < nrow)
-                    steps[(i << spr_log) + k] = live ? ck_step(from[i * nb + k]) : 0.0f;
-            }
+#pragma unroll 4
+            for (int i = first; i < nrow; i += p.stride << (5 - per_log))
+                scaled[(i << spr_log) + k] = make_float2(gamma ? ld_f32(gamma + i) : 1.0f,
+                                                         live ? ck_step(from[i * nb + k]) : 0.0f);
         } else {
             load_rows<T, V, VEC>(xtile, static_cast<const T *>(P.x) + base, P.L, left, nrow, t, p);
         }
         Pair rstd[H], neg[H];                  // neg: minus the mean
+        const float *rs = P.rstd + b * P.L + l0 + p.sub * V, *me = nullptr;
+        if constexpr (!CK)
+            me = P.mean + b * P.L + l0 + p.sub * V;
+        if constexpr (VEC) {
 #pragma unroll
-        for (int j = 0; j < V; j += 2) {
-            const int64_t l = b * P.L + l0 + p.sub * V + j;
-            const bool a = p.sub * V + j < left, c = p.sub * V + j + 1 < left;
-            rstd[j / 2] = pair(a ? __ldg(P.rstd + l) : 0.0f, c ? __ldg(P.rstd + l + 1) : 0.0f);
-            neg[j / 2] = 0;
-            if constexpr (!CK)
-                neg[j / 2] = pair(a ? -__ldg(P.mean + l) : 0.0f, c ? -__ldg(P.mean + l + 1) : 0.0f);
+            for (int j = 0; j < H; j += 2) {
+                float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), w = u;
+                if (in) {
+                    u = __ldg(reinterpret_cast<const float4 *>(rs) + j / 2);
+                    if constexpr (!CK)
+                        w = __ldg(reinterpret_cast<const float4 *>(me) + j / 2);
+                }
+                rstd[j] = pair(u.x, u.y);
+                rstd[j + 1] = pair(u.z, u.w);
+                neg[j] = pair(-w.x, -w.y);
+                neg[j + 1] = pair(-w.z, -w.w);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; j += 2) {
+                const bool u = p.sub * V + j < left, w = p.sub * V + j + 1 < left;
+                rstd[j / 2] = pair(u ? __ldg(rs + j) : 0.0f, w ? __ldg(rs + j + 1) : 0.0f);
+                neg[j / 2] = 0;
+                if constexpr (!CK)
+                    neg[j / 2] = pair(u ? -__ldg(me + j) : 0.0f, w ? -__ldg(me + j + 1) : 0.0f);
+            }
         }
-        const int my_step = (p.sub * V) / kCkBlock;
         copies_landed();
         __syncwarp();
-        // d v = gamma gy v: the checkpoint's v is h step, with one step a chunk, so h is summed
-        // and the step multiplied in once a row
+        // the checkpoint's v is h step, with one step a chunk: gamma gy v = (gy h) (gamma step)
         Pair a[H], q[H];
 #pragma unroll
         for (int j = 0; j < H; ++j)
             a[j] = q[j] = 0;
 #pragma unroll 2
-        for (int i = p.row, k = first; i < nrow; i += stride, k += hop) {
+        for (int k = 0; k < p.n; ++k) {
             Pair g[H], h[H], sg = 0, sb = 0;
-            chunk_to_pairs<T>(tile4[k], g);
-            const float w = gam[i];
-            float step = 1.0f;
+            chunk_to_pairs<T>(gmine[k * kThreads], g);
+            const float2 w = smine[k * shop];
             if constexpr (CK) {
                 uint32_t words[V / 4];
-                code_words<V>(ctile + k * V, words);
+                code_words<V>(cmine + k * kThreads * V, words);
                 codes_to_pairs<H>(words, h);
-                step = steps[(i << spr_log) + my_step];
             } else {
-                chunk_to_pairs<T>(reinterpret_cast<const uint4 *>(xtile)[k], h);
+                chunk_to_pairs<T>(xmine[k * kThreads], h);
 #pragma unroll
                 for (int j = 0; j < H; ++j)
                     h[j] = mul2(add2(h[j], neg[j]), rstd[j]);
             }
-            const Pair w2 = twice(w), ws = twice(w * step);
+            const Pair w2 = twice(w.x), ws = twice(CK ? w.x * w.y : w.x);
 #pragma unroll
             for (int j = 0; j < H; ++j) {
                 const Pair gh = mul2(g[j], h[j]);
                 a[j] = fma2(g[j], w2, a[j]);
                 q[j] = fma2(gh, ws, q[j]);
-                sg = add2(sg, gh);
-                sb = add2(sb, g[j]);
+                sg = j ? add2(sg, gh) : gh;
+                sb = j ? add2(sb, g[j]) : g[j];
             }
             if (part_g) {
                 const float2 x = halves(sg), y = halves(sb);
-                acc[k] = add2(acc[k], pair((x.x + x.y) * step, y.x + y.y));
+                Pair *to = acc + threadIdx.x + k * kThreads;
+                *to = add2(*to, pair(CK ? (x.x + x.y) * w.y : x.x + x.y, y.x + y.y));
             }
         }
-        if (!P.gx) {
-            __syncwarp();   // the next tile's copies overwrite what the warp has read
-            continue;
-        }
-        for (int o = t.lpr; o < 32; o <<= 1)
+        if (P.gx) {
 #pragma unroll
             for (int j = 0; j < H; ++j) {
-                a[j] = add2(a[j], __shfl_xor_sync(0xFFFFFFFFu, a[j], o));
-                q[j] = add2(q[j], __shfl_xor_sync(0xFFFFFFFFu, q[j], o));
+                over_rows(a[j]);
+                over_rows(q[j]);
             }
-        if (p.lane < t.lpr)
+            if (p.lane < (1 << p.lpr_log))
 #pragma unroll
-            for (int j = 0; j < H; ++j) {
-                const float2 x = halves(a[j]), y = halves(q[j]);
-                part[p.warp][p.sub * V + 2 * j] = make_float2(x.x, y.x);
-                part[p.warp][p.sub * V + 2 * j + 1] = make_float2(x.y, y.y);
-            }
-        __syncthreads();
-        float2 sum = make_float2(0.0f, 0.0f);
-        if ((int)threadIdx.x < t.tw) {
+                for (int j = 0; j < H; ++j) {
+                    const float2 x = halves(a[j]), y = halves(q[j]);
+                    part[threadIdx.x / 32][p.sub * V + 2 * j] = make_float2(x.x, y.x);
+                    part[threadIdx.x / 32][p.sub * V + 2 * j + 1] = make_float2(x.y, y.y);
+                }
+            __syncthreads();
+            const int col = threadIdx.x;
+            float2 sum = make_float2(0.0f, 0.0f);
+            if (col < t.tw) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                sum.x += part[w][threadIdx.x].x;
-                sum.y += part[w][threadIdx.x].y;
+                for (int w = 0; w < kWarps; ++w) {
+                    sum.x += part[w][col].x;
+                    sum.y += part[w][col].y;
+                }
+                own[turn][col] = sum;
             }
-            own[turn][threadIdx.x] = sum;
-        }
-        if (t.split > 1) {
-            // `own` alternates: a block writes one half while others may read the other, and
-            // passes the next barrier only after its reads of this one
-            cg::cluster_group cluster = cg::this_cluster();
-            cluster.sync();
-            if ((int)threadIdx.x < t.tw) {
-                sum = make_float2(0.0f, 0.0f);
-                for (int r = 0; r < t.split; ++r) {
-                    const float2 o = *cluster.map_shared_rank(&own[turn][threadIdx.x], r);
-                    sum.x += o.x;
-                    sum.y += o.y;
+            if (t.split > 1) {
+                // `own` alternates: a block writes one half while others may read the other,
+                // and passes the next barrier only after its reads of this one
+                cg::cluster_group cluster = cg::this_cluster();
+                cluster.sync();
+                if (col < t.tw) {
+                    sum = make_float2(0.0f, 0.0f);
+                    for (int r = 0; r < t.split; ++r) {
+                        const float2 o = *cluster.map_shared_rank(&own[turn][col], r);
+                        sum.x += o.x;
+                        sum.y += o.y;
+                    }
                 }
             }
-        }
-        if ((int)threadIdx.x < t.tw)
-            stat[threadIdx.x] = make_float2(sum.x / (float)P.C, sum.y / (float)P.C);
-        __syncthreads();
-        // grad_x = rstd gamma gy - rstd A - v rstd S
-        Pair rA[H], rS[H];
+            if (col < t.tw)
+                stat[col] = make_float2(-sum.x * t.inv_c, -sum.y * t.inv_c);
+            __syncthreads();
+            // grad_x = rstd gamma gy - rstd A - v rstd S
+            Pair rA[H], rS[H];
 #pragma unroll
-        for (int j = 0; j < H; ++j) {
-            const float2 u = stat[p.sub * V + 2 * j], w = stat[p.sub * V + 2 * j + 1];
-            rA[j] = mul2(pair(-u.x, -w.x), rstd[j]);
-            rS[j] = mul2(pair(-u.y, -w.y), rstd[j]);
-        }
-        T *out = static_cast<T *>(P.gx) + base + p.row * P.L + p.sub * V;
-#pragma unroll 2
-        for (int i = p.row, k = first; i < nrow; i += stride, k += hop, out += stride * P.L) {
-            Pair g[H], h[H];
-            chunk_to_pairs<T>(tile4[k], g);
-            const Pair w2 = twice(gam[i]);
-            if constexpr (CK) {
-                uint32_t words[V / 4];
-                code_words<V>(ctile + k * V, words);
-                codes_to_pairs<H>(words, h);
-                const Pair step = twice(steps[(i << spr_log) + my_step]);
-#pragma unroll
-                for (int j = 0; j < H; ++j)
-                    h[j] = mul2(h[j], step);
-            } else {
-                chunk_to_pairs<T>(reinterpret_cast<const uint4 *>(xtile)[k], h);
-#pragma unroll
-                for (int j = 0; j < H; ++j)
-                    h[j] = mul2(add2(h[j], neg[j]), rstd[j]);
+            for (int j = 0; j < H; ++j) {
+                const float2 u = stat[p.sub * V + 2 * j], w = stat[p.sub * V + 2 * j + 1];
+                rA[j] = mul2(pair(u.x, w.x), rstd[j]);
+                rS[j] = mul2(pair(u.y, w.y), rstd[j]);
             }
+            T *out = static_cast<T *>(P.gx) + base + p.row * P.L + p.sub * V;
+            const int64_t hop = p.stride * P.L;
+#pragma unroll 2
+            for (int k = 0; k < p.n; ++k) {
+                Pair g[H], h[H];
+                chunk_to_pairs<T>(gmine[k * kThreads], g);
+                const float2 w = smine[k * shop];
+                const Pair w2 = twice(w.x);
+                if constexpr (CK) {
+                    uint32_t words[V / 4];
+                    code_words<V>(cmine + k * kThreads * V, words);
+                    codes_to_pairs<H>(words, h);
+                    const Pair step = twice(w.y);
 #pragma unroll
-            for (int j = 0; j < H; ++j)
-                g[j] = fma2(h[j], rS[j], fma2(mul2(g[j], w2), rstd[j], rA[j]));
-            const uint4 u = pairs_to_chunk<T>(g);
-            if constexpr (!VEC)
-                tile4[k] = u;
-            else if (in)
-                *reinterpret_cast<uint4 *>(out) = u;
+                    for (int j = 0; j < H; ++j)
+                        h[j] = mul2(h[j], step);
+                } else {
+                    chunk_to_pairs<T>(xmine[k * kThreads], h);
+#pragma unroll
+                    for (int j = 0; j < H; ++j)
+                        h[j] = mul2(add2(h[j], neg[j]), rstd[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < H; ++j)
+                    g[j] = fma2(h[j], rS[j], fma2(mul2(g[j], w2), rstd[j], rA[j]));
+                const uint4 u = pairs_to_chunk<T>(g);
+                if constexpr (!VEC)
+                    tile4[threadIdx.x + k * kThreads] = u;
+                else if (in)
+                    *reinterpret_cast<uint4 *>(out) = u;
+                out += hop;
+            }
+            if constexpr (!VEC) {
+                __syncwarp();
+                store_rows<T, V>(gtile, static_cast<T *>(P.gx) + base, P.L, left, nrow, t, p);
+            }
         }
-        __syncwarp();
-        if constexpr (!VEC) {
-            store_rows(gtile, static_cast<T *>(P.gx) + base, P.L, left, nrow, t, p);
-            __syncwarp();
+        __syncwarp();   // the next tile's copies overwrite what the warp has read
+        turn ^= 1;
+        b += t.walk_b;
+        lt += t.walk_l;
+        if (lt >= tiles) {
+            lt -= tiles;
+            ++b;
         }
     }
     if (part_g) {
-        float *out = part_g + (int64_t)(blockIdx.x / t.split) * 2 * P.C + c0;
-        for (int i0 = p.warp * p.rpw, k = first; i0 < nrow; i0 += stride, k += hop) {
-            const int i = i0 + (p.lane >> t.lpr_log);
-            Pair v = i < nrow ? acc[k] : 0;
-            for (int o = 1; o < t.lpr; o <<= 1)
+        float *out = part_g + (int64_t)cluster_at * 2 * P.C + c0;
+        for (int k = 0; k < p.warp_n; ++k) {
+            Pair v = k < p.n ? acc[threadIdx.x + k * kThreads] : 0;
+            for (int o = 1; o < (1 << p.lpr_log); o <<= 1)
                 v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-            if (i < nrow && p.sub == 0) {
+            const int i = p.row + k * p.stride;
+            if (k < p.n && p.sub == 0) {
                 const float2 f = halves(v);
                 out[i] = f.x;
                 out[P.C + i] = f.y;
@@ -1001,25 +1078,25 @@ __global__ void __launch_bounds__(kThreads) norm_grad_any_kernel(const NormGrad 
     }
 }
 
-// grad_gamma[c] and grad_beta[c]: the blocks' partial sums, eight interleaved chains joined
-// in order.
+// grad_gamma[c] and grad_beta[c]: the blocks' partial sums, 32 interleaved chains (few
+// columns, so the chains are what keeps loads in flight) joined in order.
 template <class T>
-__global__ void __launch_bounds__(256) norm_weight_grad_kernel(const float *part, int64_t n,
+__global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float *part, int64_t n,
                                                                int64_t C, T *ggamma, T *gbeta) {
-    __shared__ float sums[8][33];
+    __shared__ float sums[32][33];
     const int lane = threadIdx.x & 31, group = threadIdx.x / 32;
     const int64_t i = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (i < 2 * C)
 #pragma unroll 4
-        for (int64_t j = group; j < n; j += 8)
+        for (int64_t j = group; j < n; j += 32)
             s += part[j * 2 * C + i];
     sums[group][lane] = s;
     __syncthreads();
     if (group > 0 || i >= 2 * C)
         return;
 #pragma unroll
-    for (int g = 1; g < 8; ++g)
+    for (int g = 1; g < 32; ++g)
         s += sums[g][lane];
     T *out = i < C ? ggamma : gbeta;
     if (out)
@@ -1041,7 +1118,7 @@ bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 // A block's share is at most a third of an SM's shared memory, so that three blocks are
 // there to load, reduce and store at different times; channels past that are split over a
 // cluster, and so are the channels of a tile where there are too few tiles for the SMs (at
-// least 32 channels a block, four rows a warp).
+// least as many channels a block as its threads have rows).
 template <class Bytes>
 bool make_tiling(int64_t B, int64_t C, int64_t L, int size, Bytes row_bytes, Tiling *t) {
     const int V = 16 / size;
@@ -1050,13 +1127,13 @@ bool make_tiling(int64_t B, int64_t C, int64_t L, int size, Bytes row_bytes, Til
     t->tw = V;
     while (t->tw < kRowBytes / size && t->tw < L)
         t->tw *= 2;
-    t->lpr = t->tw / V;
     t->tw_log = __builtin_ctz(t->tw);
-    t->lpr_log = __builtin_ctz(t->lpr);
-    const int rpw = 32 / t->lpr;
+    t->lpr_log = __builtin_ctz(t->tw / V);
+    t->inv_c = 1.0f / (float)C;
+    const int rows = kThreads >> t->lpr_log;   // rows of a block's threads
     t->tiles = (L + t->tw - 1) / t->tw;
     t->total = B * t->tiles;
-    auto slice = [&](int split) { return ((C + split - 1) / split + rpw - 1) / rpw * rpw; };
+    auto slice = [&](int split) { return ((C + split - 1) / split + rows - 1) / rows * rows; };
     auto shared = [&](int split) { return slice(split) * row_bytes(t->tw); };
     t->split = 1;
     while (t->split < kMaxSplit && shared(t->split) > 70 * 1024)
@@ -1064,7 +1141,7 @@ bool make_tiling(int64_t B, int64_t C, int64_t L, int size, Bytes row_bytes, Til
     if (shared(t->split) > 200 * 1024)
         return false;
     while (t->split < kMaxSplit && t->total * t->split < sm_count_or(148) &&
-           slice(t->split) >= 2 * kWarps * rpw)
+           slice(t->split) >= 2 * rows)
         t->split *= 2;
     t->slice = (int)slice(t->split);
     return t->total * t->split < (1LL << 31);
@@ -1072,8 +1149,8 @@ bool make_tiling(int64_t B, int64_t C, int64_t L, int size, Bytes row_bytes, Til
 
 // Blocks of a tile kernel that one SM holds.
 int blocks_per_sm(size_t shared) {
-    const int n = (int)((227 * 1024) / (shared + 8 * 1024));   // 8 KB: static and reserved
-    return n < 1 ? 1 : n > 3 ? 3 : n;   // 3: registers
+    const int n = (int)((227 * 1024) / (shared + 5 * 1024));   // 5 KB: static and reserved
+    return n < 1 ? 1 : n > 5 ? 5 : n;   // 5: registers
 }
 
 template <class... A>
@@ -1131,8 +1208,14 @@ cudaError_t norm(const NormProblem &P, cudaStream_t s) {
     if (make_tiling(P.B, P.C, P.L, sizeof(T), row_bytes, &t)) {
         const unsigned grid = (unsigned)(t.total * t.split);
         const size_t shared = (size_t)t.slice * row_bytes(t.tw);
-        auto kernel = vec ? (P.codes ? norm_tile_kernel<T, true, true> : norm_tile_kernel<T, true, false>)
-                          : (P.codes ? norm_tile_kernel<T, false, true> : norm_tile_kernel<T, false, false>);
+        const bool full = vec && t.lpr_log == 3;
+        auto kernel =
+            P.codes ? (full ? norm_tile_kernel<T, true, true, 3>
+                            : vec ? norm_tile_kernel<T, true, true, -1>
+                                  : norm_tile_kernel<T, false, true, -1>)
+                    : (full ? norm_tile_kernel<T, true, false, 3>
+                            : vec ? norm_tile_kernel<T, true, false, -1>
+                                  : norm_tile_kernel<T, false, false, -1>);
         return launch_cluster(kernel, grid, (unsigned)t.split, shared, s, P, t);
     }
     const int TL = lanes_along(P.L);
@@ -1156,7 +1239,8 @@ GradPlan grad_plan(const NormGrad &P) {
     GradPlan g = {};
     const int sms = sm_count_or(148);
     const bool base = aligned(P.gy, 16) && aligned(P.gx, 16) &&
-                      (P.from_codes ? aligned(P.codes, V) : aligned(P.x, 16));
+                      (P.from_codes ? aligned(P.codes, V) : aligned(P.x, 16)) &&
+                      aligned(P.rstd, 16) && aligned(P.mean, 16);
     if (P.B == 0 || P.L == 0)
         return g;
     if (P.L == 1 && base && P.C % V == 0 && aligned(P.gamma, 16)) {
@@ -1178,6 +1262,8 @@ GradPlan grad_plan(const NormGrad &P) {
         const int64_t room = (int64_t)sms * blocks_per_sm(g.shared) / g.t.split;
         g.rows = g.t.total < room ? g.t.total : room;
         g.blocks = g.rows * g.t.split;
+        g.t.walk_b = (int)(g.rows / g.t.tiles);
+        g.t.walk_l = (int)(g.rows % g.t.tiles);
         return g;
     }
     const int TL = lanes_along(P.L);
@@ -1190,8 +1276,9 @@ template <class T, bool CK>
 cudaError_t run_norm_grad(const NormGrad &P, const GradPlan &g, float *part, cudaStream_t s) {
     const unsigned grid = (unsigned)g.blocks;
     if (g.kind == 1)
-        return launch_cluster(g.vec ? norm_grad_tile_kernel<T, true, CK>
-                                    : norm_grad_tile_kernel<T, false, CK>,
+        return launch_cluster(!g.vec              ? norm_grad_tile_kernel<T, false, CK, -1>
+                              : g.t.lpr_log == 3 ? norm_grad_tile_kernel<T, true, CK, 3>
+                                                 : norm_grad_tile_kernel<T, true, CK, -1>,
                               grid, (unsigned)g.t.split, g.shared, s, P, g.t, part);
     if (g.kind >= 2) {
         auto kernel = g.kind == 2 ? (g.nv == 1   ? norm_grad_row_kernel<T, 32, 1, CK>
@@ -1221,7 +1308,7 @@ cudaError_t norm_grad(const NormGrad &P, void *ws, cudaStream_t s, int *launches
         ++*launches;
     }
     if (weights) {
-        norm_weight_grad_kernel<T><<<(unsigned)((2 * P.C + 31) / 32), 256, 0, s>>>(
+        norm_weight_grad_kernel<T><<<(unsigned)((2 * P.C + 31) / 32), 1024, 0, s>>>(
             part, g.rows, P.C, static_cast<T *>(P.ggamma), static_cast<T *>(P.gbeta));
         ++*launches;
     }
@@ -1231,8 +1318,9 @@ cudaError_t norm_grad(const NormGrad &P, void *ws, cudaStream_t s, int *launches
 // For any alignment of the tensors, so that a caller can keep the size of a shape.
 template <class T>
 size_t grad_workspace(NormGrad P) {
-    P.gamma = nullptr;
-    P.x = P.gy = P.codes = nullptr;   // aligned
+    P.gamma = P.x = P.gy = nullptr;   // aligned
+    P.codes = nullptr;
+    P.mean = P.rstd = nullptr;
     P.gx = nullptr;
     const int64_t a = grad_plan<T>(P).rows;
     P.gy = reinterpret_cast<const void *>((uintptr_t)1);
