@@ -7,13 +7,14 @@
 //   grad_gamma[c] = sum_{b,l} grad_y v,   grad_beta[c] = sum_{b,l} grad_y
 //
 // A few flops a value: the bytes bound all of it.  The normalised axis is strided by L in
-// memory, so the tile kernels keep a tile of TW positions x all channels on chip and read
-// every value once: TW * sizeof(T) = 128 bytes of each channel's row (less when L is
-// shorter), a whole DRAM burst, in shared memory.  Eight lanes hold a row, a 16-byte chunk
-// each, so a thread owns V = 16 / sizeof(T) positions and every eighth warp's rows; sums
-// over channels stay in registers until one exchange between lanes, warps and, where the
-// channels are split over the blocks of a cluster, distributed shared memory.  Each warp
-// takes its sums about its own rounded mean k, s1 = sum (x - k) and s2 = sum (x - k)^2, and
+// memory, so the tile kernels keep a tile of 32 positions x all channels in shared memory
+// and read every value once: 64 bytes (fp32: 128) of each channel's row, less when L is
+// shorter.  A thread owns 16-byte chunks, V = 16 / sizeof(T) positions of every
+// (kThreads / lanes of a row)-th channel, copies them itself, asynchronously, and needs no
+// barrier to use them; while it works on one tile the next one's copies are under way.
+// Sums over channels stay in registers until one exchange between lanes, warps and, where
+// the channels are split over the blocks of a cluster, distributed shared memory.  Each
+// warp takes its sums about a k near its mean, s1 = sum (x - k) and s2 = sum (x - k)^2, and
 // groups of n_i values are joined about a common k by
 //   s1 = sum_i s1_i + n_i d_i,  s2 = sum_i s2_i + 2 d_i s1_i + n_i d_i^2,  d_i = k_i - k:
 // one exchange instead of one for the mean and one for the variance, and no difference of
@@ -30,9 +31,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 128, kWarps = kThreads / 32;
-constexpr int kRowBytes = 128;                 // a tile's share of one channel's row, at most
-constexpr int kMaxTW = kRowBytes / 2;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kTW = 32;                        // positions of a tile, at most; a block of codes
 constexpr int kMaxSplit = 8;                   // blocks of a portable cluster
 
 // How a launch cuts [B, C, L] into tiles.
@@ -82,6 +82,13 @@ __device__ __forceinline__ void copy_async(void *dst, const void *src, bool in) 
 
 __device__ __forceinline__ void copies_landed() {
     asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// All but the last group issued.
+__device__ __forceinline__ void earlier_copies_landed() {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
 }
 
 // Where a thread stands in its block's tile.  Chunk k of a tile is row k / lpr, part k % lpr;
@@ -212,455 +219,511 @@ __device__ __forceinline__ void put_code_words(int8_t *p, const uint32_t (&w)[V 
         *reinterpret_cast<uint32_t *>(p) = w[0];
 }
 
+// v[i], i < 2H, summed over the lanes that hold the same positions, into part[2][TW] in
+// shared memory: the first H for row 0, the others for row 1.  Full rows: by halving
+// exchanges (a shuffle for each value that leaves), after which each lane has its share.
+template <int H, int LPR_LOG, int TW = kTW>
+__device__ __forceinline__ void put_row_sums(Pair (&v)[2 * H], float *part, int lpr_log, int lane,
+                                             int sub) {
+    constexpr int V = 2 * H;
+    if constexpr (LPR_LOG >= 0) {
+        // RL lanes hold the same positions; each ends with N = 2H / RL neighbouring sums
+        constexpr int RL = 32 >> LPR_LOG, N = 2 * H / RL;
+        static_assert(N >= 1 && N * RL == 2 * H, "whole sums a lane");
+        const int rl = lane >> LPR_LOG;
+#pragma unroll
+        for (int m = RL / 2; m >= 1; m >>= 1) {
+            const bool upper = rl & m;
+#pragma unroll
+            for (int j = 0; j < m * N; ++j) {
+                const Pair send = upper ? v[j] : v[j + m * N], keep = upper ? v[j + m * N] : v[j];
+                v[j] = add2(keep, __shfl_xor_sync(0xFFFFFFFFu, send, m << LPR_LOG));
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int i = rl * N + j;
+            *reinterpret_cast<float2 *>(part + (i >= H ? TW : 0) + sub * V + 2 * (i & (H - 1))) =
+                halves(v[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 2 * H; ++j) {
+            for (int o = 1 << lpr_log; o < 32; o <<= 1)
+                v[j] = add2(v[j], __shfl_xor_sync(0xFFFFFFFFu, v[j], o));
+            if (lane < (1 << lpr_log)) {
+                const float2 f = halves(v[j]);
+                float *to = part + (j >= H ? TW : 0) + sub * V + 2 * (j & (H - 1));
+                to[0] = f.x;
+                to[1] = f.y;
+            }
+        }
+    }
+}
+
+// Sum over eight consecutive lanes.
+__device__ __forceinline__ float sum8(float v) {
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
 // Sums of a group of n values about k.
 struct Moments {
     float k, s1, s2;
 };
 
-// `count` groups (at(i) and size(i), the first not empty) joined about their common mean,
-// rounded.
-template <int COUNT, class At, class Size>
-__device__ __forceinline__ Moments join(At at, Size size) {
-    const float k0 = at(0).k;
-    float n = 0.0f, sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-        const Moments m = at(i);
-        const float c = size(i);
-        n += c;
-        if (c > 0.0f)
-            sum += fmaf(c, m.k - k0, m.s1);
-    }
-    Moments r{k0 + sum / fmaxf(n, 1.0f), 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-        const Moments m = at(i);
-        const float c = size(i);
-        if (c > 0.0f) {
-            const float d = m.k - r.k;
-            r.s1 += fmaf(c, d, m.s1);
-            r.s2 += fmaf(d, fmaf(c, d, 2.0f * m.s1), m.s2);
-        }
-    }
-    return r;
+// A group of n values a lane of eight (n may be 0, but not in the first lane), joined about
+// their common mean, rounded; in every lane.
+__device__ __forceinline__ Moments join8(Moments m, float n) {
+    const float k0 = __shfl_sync(0xFFFFFFFFu, m.k, threadIdx.x & 24);
+    const bool some = n > 0.0f;
+    const float all = sum8(n), k = k0 + sum8(some ? fmaf(n, m.k - k0, m.s1) : 0.0f) / fmaxf(all, 1.0f);
+    const float d = m.k - k;
+    return Moments{k, sum8(some ? fmaf(n, d, m.s1) : 0.0f),
+                   sum8(some ? fmaf(d, fmaf(n, d, 2.0f * m.s1), m.s2) : 0.0f)};
 }
 
+// A walk of the clusters of a launch over the tiles.
+struct Walk {
+    int64_t b;
+    unsigned lt;
+    __device__ Walk(const Tiling &t, unsigned at) {
+        b = at / (unsigned)t.tiles;
+        lt = at - (unsigned)b * (unsigned)t.tiles;
+    }
+    __device__ void step(const Tiling &t) {
+        b += t.walk_b;
+        lt += t.walk_l;
+        if (lt >= (unsigned)t.tiles) {
+            lt -= (unsigned)t.tiles;
+            ++b;
+        }
+    }
+};
+
+constexpr int kFirstRows = 4;   // rows of a lane that give its warp's k
+
 template <class T, bool VEC, bool CK, int LPR_LOG>
-__global__ void __launch_bounds__(kThreads) norm_tile_kernel(const NormProblem P, const Tiling t) {
+__global__ void __launch_bounds__(kThreads, 3) norm_tile_kernel(const NormProblem P,
+                                                                const Tiling t) {
     constexpr int V = Vec<T>::V, H = Vec<T>::H;
-    extern __shared__ uint4 tile4[];           // chunks of the slice; !VEC: then its codes
-    __shared__ Moments part[kWarps][kMaxTW];   // of a warp's rows, a position
-    __shared__ float count[kWarps];
-    __shared__ Moments own[kMaxTW];            // of the block's rows (cluster)
-    __shared__ float2 stat[kMaxTW];            // (-mean, rstd)
-    T *tile = reinterpret_cast<T *>(tile4);
+    extern __shared__ uint4 tile4[];           // VEC: two tiles; else one, then its codes
+    __shared__ __align__(8) float part[kWarps][2 * kTW], part_k[kWarps][kTW], count[kWarps];
+    __shared__ Moments own[2][kTW];            // of the block's rows (cluster)
+    __shared__ float2 stat[kTW];               // (-mean, rstd)
     const int rank = t.split > 1 ? blockIdx.x % t.split : 0;
-    const unsigned at = t.split > 1 ? blockIdx.x / t.split : blockIdx.x;
-    const unsigned tiles = (unsigned)t.tiles, bu = at / tiles;
-    const int64_t b = bu, l0 = (int64_t)(at - bu * tiles) << t.tw_log;
-    const int64_t left = P.L - l0;             // positions of this tile (tw or more: all)
+    Walk w(t, t.split > 1 ? blockIdx.x / t.split : blockIdx.x), ahead = w;
     const int c0 = rank * t.slice;
     const int nrow = min(t.slice, (int)P.C - c0);   // may be 0 or less in the last blocks
     const Place<LPR_LOG> p(t, nrow);
-    int8_t *ctile = reinterpret_cast<int8_t *>(tile4 + (t.slice << p.lpr_log));
-    const int64_t base = (b * P.C + c0) * P.L + l0;
-    load_rows<T, V, VEC>(tile, static_cast<const T *>(P.x) + base, P.L, left, nrow, t, p);
-    copies_landed();
-    __syncwarp();
-
-    uint4 *mine = tile4 + threadIdx.x;
-    Pair f[H], s[H];
-#pragma unroll
-    for (int j = 0; j < H; ++j)
-        s[j] = 0;
-#pragma unroll 4
-    for (int k = 0; k < p.n; ++k) {
-        chunk_to_pairs<T>(mine[k * kThreads], f);
-#pragma unroll
-        for (int j = 0; j < H; ++j)
-            s[j] = add2(s[j], f[j]);
-    }
-    auto over_rows = [&](Pair &v) {            // the lanes that hold the same positions
-        if constexpr (LPR_LOG >= 0) {
-#pragma unroll
-            for (int o = 1 << LPR_LOG; o < 32; o <<= 1)
-                v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-        } else {
-            for (int o = 1 << p.lpr_log; o < 32; o <<= 1)
-                v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-        }
-    };
-    int rows = p.n;
-    for (int o = 1 << p.lpr_log; o < 32; o <<= 1)
-        rows += __shfl_xor_sync(0xFFFFFFFFu, rows, o);
-    const Pair over = twice(rows > 0 ? -1.0f / (float)rows : 0.0f);
-    Pair neg[H], s1[H];                        // neg: minus the warp's mean
-#pragma unroll
-    for (int j = 0; j < H; ++j) {
-        over_rows(s[j]);
-        neg[j] = mul2(s[j], over);
-        s1[j] = s[j] = 0;
-    }
-#pragma unroll 4
-    for (int k = 0; k < p.n; ++k) {
-        chunk_to_pairs<T>(mine[k * kThreads], f);
-#pragma unroll
-        for (int j = 0; j < H; ++j) {
-            const Pair d = add2(f[j], neg[j]);
-            s1[j] = add2(s1[j], d);
-            s[j] = fma2(d, d, s[j]);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < H; ++j) {
-        over_rows(s1[j]);
-        over_rows(s[j]);
-    }
-    if (p.lane < (1 << p.lpr_log)) {
-#pragma unroll
-        for (int j = 0; j < H; ++j) {
-            const float2 k = halves(neg[j]), u = halves(s1[j]), w = halves(s[j]);
-            part[threadIdx.x / 32][p.sub * V + 2 * j] = Moments{-k.x, u.x, w.x};
-            part[threadIdx.x / 32][p.sub * V + 2 * j + 1] = Moments{-k.y, u.y, w.y};
-        }
-        if (p.lane == 0)
-            count[threadIdx.x / 32] = (float)rows;
-    }
-    __syncthreads();
-    const int col = threadIdx.x;
-    Moments m{0.0f, 0.0f, 0.0f};
-    if (col < t.tw) {
-        m = join<kWarps>([&](int w) { return part[w][col]; }, [&](int w) { return count[w]; });
-        own[col] = m;
-    }
-    if (t.split > 1) {
-        cg::cluster_group cluster = cg::this_cluster();
-        cluster.sync();
-        if (col < t.tw) {
-            Moments o[kMaxSplit];
-#pragma unroll
-            for (int r = 0; r < kMaxSplit; ++r)
-                o[r] = *cluster.map_shared_rank(&own[col], min(r, t.split - 1));
-            m = join<kMaxSplit>(
-                [&](int r) { return o[r]; },
-                [&](int r) {
-                    return r < t.split ? (float)max(0, min(t.slice, (int)P.C - r * t.slice)) : 0.0f;
-                });
-        }
-    }
-    if (col < t.tw) {
-        const float off = m.s1 * t.inv_c, var = fmaxf(m.s2 * t.inv_c - off * off, 0.0f);
-        const float rstd = 1.0f / sqrtf((m.s2 == m.s2 ? var : m.s2) + P.eps);   // fmaxf drops NaN
-        stat[col] = make_float2(-(m.k + off), rstd);
-        if (rank == 0 && col < left) {
-            if (P.mean)
-                P.mean[b * P.L + l0 + col] = m.k + off;
-            if (P.rstd)
-                P.rstd[b * P.L + l0 + col] = rstd;
-        }
-    }
-    __syncthreads();
-
-    Pair rstd[H];
-#pragma unroll
-    for (int j = 0; j < H; ++j) {
-        const float2 u = stat[p.sub * V + 2 * j], w = stat[p.sub * V + 2 * j + 1];
-        neg[j] = pair(u.x, w.x);
-        rstd[j] = pair(u.y, w.y);
-    }
-    const bool in = p.sub * V < left;
+    const int chunks = t.slice << p.lpr_log;   // of a tile
+    int8_t *ctile = reinterpret_cast<int8_t *>(tile4 + chunks);
     const int64_t nb = ck_blocks(P.L);
     const int lanes = min(kCkBlock / V, 1 << p.lpr_log);   // lanes of a block of 32 values
     const T *gamma = P.gamma ? static_cast<const T *>(P.gamma) + c0 + p.row : nullptr;
     const T *beta = P.beta ? static_cast<const T *>(P.beta) + c0 + p.row : nullptr;
-    T *y = static_cast<T *>(P.y) + base + p.row * P.L + p.sub * V;
-    int8_t *codes = P.codes + base + p.row * P.L + p.sub * V;
-    uint8_t *scale = P.scales + (b * P.C + c0 + p.row) * nb + (l0 + p.sub * V) / kCkBlock;
     const int64_t hop = p.stride * P.L, scale_hop = p.stride * nb;
-    // CK: whole warps walk together, for the block maximum's shuffles
-    const int n = CK ? p.warp_n : p.n;
-#pragma unroll 2
-    for (int k = 0; k < n; ++k) {
-        const bool row = !CK || k < p.n;
-        Pair v[H];
-        chunk_to_pairs<T>(mine[k * kThreads], v);   // rows past nrow: inside the tile, not used
-        const Pair g = twice(gamma && row ? ld_f32(gamma + k * p.stride) : 1.0f);
-        const Pair be = twice(beta && row ? ld_f32(beta + k * p.stride) : 0.0f);
+    auto load = [&](const Walk &at, int stage) {
+        const int64_t l0 = (int64_t)at.lt << t.tw_log;
+        load_rows<T, V, VEC>(reinterpret_cast<T *>(tile4 + stage * chunks),
+                             static_cast<const T *>(P.x) + (at.b * P.C + c0) * P.L + l0, P.L,
+                             P.L - l0, nrow, t, p);
+    };
+    if (p.lane == 0) {
+        const int first = (int)threadIdx.x >> p.lpr_log, rows = 32 >> p.lpr_log;
+        int n = 0;                             // rows of the warp
+        for (int i = first; i < nrow; i += p.stride)
+            n += min(rows, nrow - i);
+        count[threadIdx.x / 32] = (float)n;
+    }
+    if constexpr (VEC) {
+        load(w, 0);
+        copies_issued();
+    }
+    int turn = 0;
+    for (; w.b < P.B; w.step(t), turn ^= 1) {
+        const int64_t l0 = (int64_t)w.lt << t.tw_log;
+        const int64_t left = P.L - l0;         // positions of this tile (tw or more: all)
+        const int64_t base = (w.b * P.C + c0) * P.L + l0;
+        const int stage = VEC ? turn : 0;
+        if constexpr (VEC) {
+            ahead.step(t);
+            if (ahead.b < P.B)
+                load(ahead, stage ^ 1);
+            copies_issued();
+            earlier_copies_landed();
+        } else {
+            load(w, 0);
+            copies_landed();
+            __syncwarp();
+        }
+        uint4 *mine = tile4 + stage * chunks + threadIdx.x;
+        // k: the mean of the first rows of the warp's first lane of each position
+        Pair f[H], k[H], s[2 * H];
+        const int first = min(p.n, kFirstRows);
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+            k[j] = 0;
+#pragma unroll
+        for (int r = 0; r < kFirstRows; ++r)
+            if (r < first) {
+                chunk_to_pairs<T>(mine[r * kThreads], f);
+#pragma unroll
+                for (int j = 0; j < H; ++j)
+                    k[j] = add2(k[j], f[j]);
+            }
+        const Pair over = twice(first > 0 ? -1.0f / (float)first : 0.0f);
 #pragma unroll
         for (int j = 0; j < H; ++j) {
-            v[j] = mul2(add2(v[j], neg[j]), rstd[j]);
-            f[j] = fma2(v[j], g, be);
+            k[j] = __shfl_sync(0xFFFFFFFFu, mul2(k[j], over), p.sub);   // minus k
+            s[j] = s[H + j] = 0;
         }
-        const uint4 o = pairs_to_chunk<T>(f);
-        if constexpr (!VEC) {
-            if (row)
-                mine[k * kThreads] = o;
-        } else {
-            if (row && in)
-                *reinterpret_cast<uint4 *>(y) = o;
-            y += hop;
-        }
-        if constexpr (CK) {
-            float top = 0.0f;
+#pragma unroll 4
+        for (int r = 0; r < p.n; ++r) {
+            chunk_to_pairs<T>(mine[r * kThreads], f);
 #pragma unroll
             for (int j = 0; j < H; ++j) {
-                float2 a = halves(v[j]);
-                if constexpr (!VEC) {          // values past the row's end
-                    a.x = p.sub * V + 2 * j < left ? a.x : 0.0f;
-                    a.y = p.sub * V + 2 * j + 1 < left ? a.y : 0.0f;
-                    v[j] = pair(a.x, a.y);
-                }
-                top = max_abs(max_abs(top, a.x), a.y);
+                const Pair d = add2(f[j], k[j]);
+                s[j] = add2(s[j], d);
+                s[H + j] = fma2(d, d, s[H + j]);
             }
-            uint32_t bits = row && in ? ck_abs_bits(top) : 0u;
-            if constexpr (LPR_LOG >= 0) {
-#pragma unroll
-                for (int o2 = 1; o2 < kCkBlock / V && o2 < (1 << LPR_LOG); o2 <<= 1)
-                    bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o2));
-            } else {
-                for (int o2 = 1; o2 < lanes; o2 <<= 1)
-                    bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o2));
-            }
-            const uint32_t e = ck_scale(bits, ck_top<float>());
-            uint32_t w[V / 4];
-            code_pairs<H>(v, ck_inverse(e), w);
-            if constexpr (!VEC)
-                put_code_words<V>(ctile + (threadIdx.x + k * kThreads) * V, w);
-            else if (row && in)
-                put_code_words<V>(codes, w);
-            if (row && in && (p.sub & (lanes - 1)) == 0)
-                *scale = (uint8_t)e;
-            codes += hop;
-            scale += scale_hop;
         }
-    }
-    if constexpr (!VEC) {
-        __syncwarp();
-        store_rows<T, V>(tile, static_cast<T *>(P.y) + base, P.L, left, nrow, t, p);
-        if constexpr (CK)
-            store_rows<int8_t, V>(ctile, P.codes + base, P.L, left, nrow, t, p);
+        put_row_sums<H, LPR_LOG>(s, part[threadIdx.x / 32], p.lpr_log, p.lane, p.sub);
+        if (p.lane < (1 << p.lpr_log))
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                const float2 u = halves(k[j]);
+                part_k[threadIdx.x / 32][p.sub * V + 2 * j] = -u.x;
+                part_k[threadIdx.x / 32][p.sub * V + 2 * j + 1] = -u.y;
+            }
+        __syncthreads();
+        {   // eight threads a position, one a warp's sums
+            static_assert(kThreads == 8 * kTW && kWarps == 8, "a thread for each warp and position");
+            const int col = threadIdx.x / 8, g = threadIdx.x % 8;
+            Moments m = join8(Moments{part_k[g][col], part[g][col], part[g][kTW + col]}, count[g]);
+            if (t.split > 1) {
+                cg::cluster_group cluster = cg::this_cluster();
+                if (g == 0)
+                    own[turn][col] = m;
+                cluster.sync();
+                // `own` alternates: a block writes one half while others may read the other,
+                // and passes the next barrier only after its reads of this one
+                static_assert(kMaxSplit == 8, "a thread for each block");
+                if (g < t.split)
+                    m = *cluster.map_shared_rank(&own[turn][col], g);
+                m = join8(m, g < t.split ? (float)max(0, min(t.slice, (int)P.C - g * t.slice)) : 0.0f);
+            }
+            const float off = m.s1 * t.inv_c, var = fmaxf(m.s2 * t.inv_c - off * off, 0.0f);
+            const float rstd = 1.0f / sqrtf((m.s2 == m.s2 ? var : m.s2) + P.eps);   // fmaxf drops NaN
+            if (g == 0) {
+                stat[col] = make_float2(-(m.k + off), rstd);
+                if (rank == 0 && col < min((int64_t)t.tw, left)) {
+                    if (P.mean)
+                        P.mean[w.b * P.L + l0 + col] = m.k + off;
+                    if (P.rstd)
+                        P.rstd[w.b * P.L + l0 + col] = rstd;
+                }
+            }
+        }
+        __syncthreads();
+        Pair rstd[H];
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            const float2 u = stat[p.sub * V + 2 * j], v = stat[p.sub * V + 2 * j + 1];
+            k[j] = pair(u.x, v.x);
+            rstd[j] = pair(u.y, v.y);
+        }
+        const bool in = p.sub * V < left;
+        T *y = static_cast<T *>(P.y) + base + p.row * P.L + p.sub * V;
+        int8_t *codes = P.codes + base + p.row * P.L + p.sub * V;
+        uint8_t *scale = P.scales + (w.b * P.C + c0 + p.row) * nb + l0 / kCkBlock;
+        // CK: whole warps walk together, for the block maximum's shuffles
+        const int n = CK ? p.warp_n : p.n;
+#pragma unroll 2
+        for (int r = 0; r < n; ++r) {
+            const bool row = !CK || r < p.n;
+            Pair v[H];
+            chunk_to_pairs<T>(mine[r * kThreads], v);   // rows past nrow: inside the tile, not used
+            const Pair g = twice(gamma && row ? ld_f32(gamma + r * p.stride) : 1.0f);
+            const Pair be = twice(beta && row ? ld_f32(beta + r * p.stride) : 0.0f);
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                v[j] = mul2(add2(v[j], k[j]), rstd[j]);
+                f[j] = fma2(v[j], g, be);
+            }
+            const uint4 o = pairs_to_chunk<T>(f);
+            if constexpr (!VEC) {
+                if (row)
+                    mine[r * kThreads] = o;
+            } else {
+                if (row && in)
+                    *reinterpret_cast<uint4 *>(y) = o;
+                y += hop;
+            }
+            if constexpr (CK) {
+                float top = 0.0f;
+#pragma unroll
+                for (int j = 0; j < H; ++j) {
+                    float2 a = halves(v[j]);
+                    if constexpr (!VEC) {      // values past the row's end
+                        a.x = p.sub * V + 2 * j < left ? a.x : 0.0f;
+                        a.y = p.sub * V + 2 * j + 1 < left ? a.y : 0.0f;
+                        v[j] = pair(a.x, a.y);
+                    }
+                    top = max_abs(max_abs(top, a.x), a.y);
+                }
+                uint32_t bits = row && in ? ck_abs_bits(top) : 0u;
+                if constexpr (LPR_LOG >= 0) {
+#pragma unroll
+                    for (int o2 = 1; o2 < (1 << LPR_LOG); o2 <<= 1)
+                        bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o2));
+                } else {
+                    for (int o2 = 1; o2 < lanes; o2 <<= 1)
+                        bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o2));
+                }
+                const uint32_t e = ck_scale(bits, ck_top<float>());
+                uint32_t q[V / 4];
+                code_pairs<H>(v, ck_inverse(e), q);
+                if constexpr (!VEC)
+                    put_code_words<V>(ctile + (threadIdx.x + r * kThreads) * V, q);
+                else if (row && in)
+                    put_code_words<V>(codes, q);
+                if (row && p.sub == 0)
+                    *scale = (uint8_t)e;
+                codes += hop;
+                scale += scale_hop;
+            }
+        }
+        if constexpr (!VEC) {
+            __syncwarp();
+            store_rows<T, V>(reinterpret_cast<T *>(tile4), static_cast<T *>(P.y) + base, P.L, left,
+                             nrow, t, p);
+            if constexpr (CK)
+                store_rows<int8_t, V>(ctile, P.codes + base, P.L, left, nrow, t, p);
+            __syncwarp();   // the next tile's values overwrite what the warp has read
+        }
     }
     if (t.split > 1)
         cg::this_cluster().sync();   // another block may still read this one's `own`
 }
 
-// Shared memory of the gradient's tile kernel for a channel: grad_y and x (or codes), each
-// lane's sums of grad_y v and grad_y of its rows, and gamma with the steps of the codes.
+// Shared memory of the forward's tile kernel for a channel: two tiles, or one and its codes.
 template <class T>
-constexpr int grad_row_bytes(int tw, bool ck) {
-    const int V = 16 / (int)sizeof(T), steps = ck && tw > kCkBlock ? tw / kCkBlock : 1;
-    return tw * (int)sizeof(T) + tw * (ck ? 1 : (int)sizeof(T)) + tw / V * 8 + steps * 8;
+constexpr int norm_row_bytes(int tw, bool vec, bool ck) {
+    return tw * (vec ? 2 * (int)sizeof(T) : (int)sizeof(T) + (ck ? 1 : 0));
 }
+
+// The same of the gradient's: grad_y and x (or codes) of two tiles or one, each lane's sums
+// of grad_y v and grad_y of its rows, and gamma with the step of the codes.
+template <class T>
+constexpr int grad_row_bytes(int tw, bool vec, bool ck) {
+    const int V = 16 / (int)sizeof(T);
+    return (vec ? 2 : 1) * tw * ((int)sizeof(T) + (ck ? 1 : (int)sizeof(T))) + tw / V * 8 + 8;
+}
+
+constexpr int kStepRegs = 4;   // step bytes a lane holds of the next tile
+constexpr int kMaxSlice = kStepRegs * kThreads;
 
 // grad_x tile by tile.  A cluster of t.split blocks walks tiles cluster, cluster + n, ...;
 // each lane's sums of grad_y v and grad_y over its rows and the walk stay in shared memory
 // (one addition a row and tile instead of a shuffle tree) and are joined at the end into
 // the cluster's rows of `part_g` [clusters][2][C]: a fixed order, no atomics.
 template <class T, bool VEC, bool CK, int LPR_LOG>
-__global__ void __launch_bounds__(kThreads, 5) norm_grad_tile_kernel(const NormGrad P,
+__global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormGrad P,
                                                                      const Tiling t,
                                                                      float *part_g) {
-    constexpr int V = Vec<T>::V, H = Vec<T>::H;
-    extern __shared__ uint4 tile4[];           // chunks of grad_y, then of x / codes
-    __shared__ float2 part[kWarps][kMaxTW];
-    __shared__ float2 own[2][kMaxTW];
-    __shared__ float2 stat[kMaxTW];            // (-A, -S)
+    constexpr int V = Vec<T>::V, H = Vec<T>::H, STAGES = VEC ? 2 : 1;
+    extern __shared__ uint4 tile4[];           // chunks of grad_y, then of x / codes, by stages
+    __shared__ __align__(8) float part[kWarps][2 * kTW];
+    __shared__ float2 own[2][kTW];
+    __shared__ float2 stat[kTW];               // (-A, -S)
     const int rank = t.split > 1 ? blockIdx.x % t.split : 0;
     const unsigned cluster_at = t.split > 1 ? blockIdx.x / t.split : blockIdx.x;
+    Walk w(t, cluster_at), ahead = w;
     const int c0 = rank * t.slice;
     const int nrow = min(t.slice, (int)P.C - c0);
     const Place<LPR_LOG> p(t, nrow);
+    const int chunks = t.slice << p.lpr_log;   // of a tile
     T *gtile = reinterpret_cast<T *>(tile4);
-    unsigned char *at_byte = reinterpret_cast<unsigned char *>(tile4 + (t.slice << p.lpr_log));
-    T *xtile = reinterpret_cast<T *>(at_byte);
-    int8_t *ctile = reinterpret_cast<int8_t *>(at_byte);
-    at_byte += ((size_t)t.slice << t.tw_log) * (CK ? 1 : sizeof(T));
-    Pair *acc = reinterpret_cast<Pair *>(at_byte);         // a chunk
-    at_byte += ((size_t)t.slice << p.lpr_log) * sizeof(Pair);
-    float2 *scaled = reinterpret_cast<float2 *>(at_byte);  // [slice][spr]: gamma, step
-    const int spr_log = CK ? max(t.tw_log - 5, 0) : 0, spr = 1 << spr_log;   // steps of a row
+    uint4 *after = tile4 + STAGES * chunks;
+    T *xtile = reinterpret_cast<T *>(after);
+    int8_t *ctile = reinterpret_cast<int8_t *>(after);
+    unsigned char *at_byte = reinterpret_cast<unsigned char *>(after) +
+                             (size_t)STAGES * chunks * V * (CK ? 1 : sizeof(T));
+    Pair *acc = reinterpret_cast<Pair *>(at_byte);                    // a chunk
+    float2 *scaled = reinterpret_cast<float2 *>(acc + chunks);        // a row: gamma, step
     const int64_t nb = ck_blocks(P.L);
     const T *gamma = P.gamma ? static_cast<const T *>(P.gamma) + c0 : nullptr;
-    for (int k = 0; k < p.n; ++k) {
-        acc[threadIdx.x + k * kThreads] = 0;
-        const int i = p.row + k * p.stride;
-        if (!CK && p.sub == 0)
-            scaled[i] = make_float2(gamma ? ld_f32(gamma + i) : 1.0f, 1.0f);
-    }
-    const uint4 *gmine = tile4 + threadIdx.x;
-    const int8_t *cmine = ctile + threadIdx.x * V;
-    const uint4 *xmine = reinterpret_cast<const uint4 *>(xtile) + threadIdx.x;
-    const float2 *smine = scaled + (p.row << spr_log) + (CK ? (p.sub * V) / kCkBlock : 0);
-    const int shop = p.stride << spr_log;
-    auto over_rows = [&](Pair &v) {            // the lanes that hold the same positions
-        if constexpr (LPR_LOG >= 0) {
+    // the warp's rows, one a lane: rows first, first + rows_hop, ... are this lane's to fetch
+    // gamma and the steps of
+    const int rows_log = 5 - p.lpr_log;
+    const int first = ((int)(threadIdx.x & ~31u) >> p.lpr_log) + (p.lane >> rows_log) * p.stride +
+                      (p.lane & ((1 << rows_log) - 1));
+    const int rows_hop = p.stride << p.lpr_log;
+    for (int r = 0; r < p.n; ++r)
+        acc[threadIdx.x + r * kThreads] = 0;
+    for (int i = first; i < nrow; i += rows_hop)
+        scaled[i] = make_float2(gamma ? ld_f32(gamma + i) : 1.0f, 1.0f);
+    uint8_t step[kStepRegs] = {};
+    auto load = [&](const Walk &at, int stage) {
+        const int64_t l0 = (int64_t)at.lt << t.tw_log, base = (at.b * P.C + c0) * P.L + l0;
+        load_rows<T, V, VEC>(gtile + stage * chunks * V, static_cast<const T *>(P.gy) + base, P.L,
+                             P.L - l0, nrow, t, p);
+        if constexpr (CK) {
+            load_rows<int8_t, V, VEC>(ctile + stage * chunks * V, P.codes + base, P.L, P.L - l0,
+                                      nrow, t, p);
+            const uint8_t *from = P.scales + (at.b * P.C + c0) * nb + l0 / kCkBlock;
 #pragma unroll
-            for (int o = 1 << LPR_LOG; o < 32; o <<= 1)
-                v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+            for (int r = 0; r < kStepRegs; ++r)
+                if (first + r * rows_hop < nrow)
+                    step[r] = from[(first + r * rows_hop) * nb];
         } else {
-            for (int o = 1 << p.lpr_log; o < 32; o <<= 1)
-                v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+            load_rows<T, V, VEC>(xtile + stage * chunks * V, static_cast<const T *>(P.x) + base,
+                                 P.L, P.L - l0, nrow, t, p);
         }
     };
+    if constexpr (VEC) {
+        load(w, 0);
+        copies_issued();
+    }
     int turn = 0;
-    const unsigned tiles = (unsigned)t.tiles;
-    int64_t b = cluster_at / tiles;
-    unsigned lt = cluster_at - (unsigned)b * tiles;
-    while (b < P.B) {
-        const int64_t l0 = (int64_t)lt << t.tw_log;
+    for (; w.b < P.B; w.step(t), turn ^= 1) {
+        const int64_t l0 = (int64_t)w.lt << t.tw_log;
         const int64_t left = P.L - l0;
-        const int64_t base = (b * P.C + c0) * P.L + l0;
+        const int64_t base = (w.b * P.C + c0) * P.L + l0;
         const bool in = p.sub * V < left;
-        load_rows<T, V, VEC>(gtile, static_cast<const T *>(P.gy) + base, P.L, left, nrow, t, p);
-        if constexpr (CK) {
-            load_rows<int8_t, V, VEC>(ctile, P.codes + base, P.L, left, nrow, t, p);
-            // gamma and the steps of the warp's rows, one of each a lane
-            const int per_log = spr_log + 5 - p.lpr_log;   // log2 of the steps of a warp's rows
-            const uint8_t *from = P.scales + (b * P.C + c0) * nb + l0 / kCkBlock;
-            const int k = p.lane & (spr - 1);
-            const bool live = l0 / kCkBlock + k < nb;
-            const int first = ((int)(threadIdx.x & ~31u) >> p.lpr_log) +
-                              (p.lane >> per_log) * p.stride +
-                              ((p.lane & ((1 << per_log) - 1)) >> spr_log);
-#pragma unroll 4
-            for (int i = first; i < nrow; i += p.stride << (5 - per_log))
-                scaled[(i << spr_log) + k] = make_float2(gamma ? ld_f32(gamma + i) : 1.0f,
-                                                         live ? ck_step(from[i * nb + k]) : 0.0f);
-        } else {
-            load_rows<T, V, VEC>(xtile, static_cast<const T *>(P.x) + base, P.L, left, nrow, t, p);
-        }
+        const int stage = VEC ? turn : 0;
+        if constexpr (!VEC)
+            load(w, 0);
+        if constexpr (CK)                      // every lane has read the last tile's steps
+#pragma unroll
+            for (int r = 0; r < kStepRegs; ++r)
+                if (first + r * rows_hop < nrow)
+                    scaled[first + r * rows_hop].y = ck_step(step[r]);
         Pair rstd[H], neg[H];                  // neg: minus the mean
-        const float *rs = P.rstd + b * P.L + l0 + p.sub * V, *me = nullptr;
+        const float *rs = P.rstd + w.b * P.L + l0 + p.sub * V, *me = nullptr;
         if constexpr (!CK)
-            me = P.mean + b * P.L + l0 + p.sub * V;
+            me = P.mean + w.b * P.L + l0 + p.sub * V;
         if constexpr (VEC) {
 #pragma unroll
             for (int j = 0; j < H; j += 2) {
-                float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), w = u;
+                float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = u;
                 if (in) {
                     u = __ldg(reinterpret_cast<const float4 *>(rs) + j / 2);
                     if constexpr (!CK)
-                        w = __ldg(reinterpret_cast<const float4 *>(me) + j / 2);
+                        v = __ldg(reinterpret_cast<const float4 *>(me) + j / 2);
                 }
                 rstd[j] = pair(u.x, u.y);
                 rstd[j + 1] = pair(u.z, u.w);
-                neg[j] = pair(-w.x, -w.y);
-                neg[j + 1] = pair(-w.z, -w.w);
+                neg[j] = pair(-v.x, -v.y);
+                neg[j + 1] = pair(-v.z, -v.w);
             }
+            ahead.step(t);
+            if (ahead.b < P.B)
+                load(ahead, stage ^ 1);
+            copies_issued();
+            earlier_copies_landed();
         } else {
 #pragma unroll
             for (int j = 0; j < V; j += 2) {
-                const bool u = p.sub * V + j < left, w = p.sub * V + j + 1 < left;
-                rstd[j / 2] = pair(u ? __ldg(rs + j) : 0.0f, w ? __ldg(rs + j + 1) : 0.0f);
+                const bool u = p.sub * V + j < left, v = p.sub * V + j + 1 < left;
+                rstd[j / 2] = pair(u ? __ldg(rs + j) : 0.0f, v ? __ldg(rs + j + 1) : 0.0f);
                 neg[j / 2] = 0;
                 if constexpr (!CK)
-                    neg[j / 2] = pair(u ? -__ldg(me + j) : 0.0f, w ? -__ldg(me + j + 1) : 0.0f);
+                    neg[j / 2] = pair(u ? -__ldg(me + j) : 0.0f, v ? -__ldg(me + j + 1) : 0.0f);
             }
+            copies_landed();
         }
-        copies_landed();
         __syncwarp();
-        // the checkpoint's v is h step, with one step a chunk: gamma gy v = (gy h) (gamma step)
-        Pair a[H], q[H];
+        const uint4 *gmine = tile4 + stage * chunks + threadIdx.x;
+        const int8_t *cmine = ctile + (stage * chunks + threadIdx.x) * V;
+        const uint4 *xmine = reinterpret_cast<const uint4 *>(xtile) + stage * chunks + threadIdx.x;
+        const float2 *smine = scaled + p.row;
+        // the checkpoint's v is h step, with one step a row: gamma gy v = (gy h) (gamma step)
+        Pair s[2 * H];
 #pragma unroll
-        for (int j = 0; j < H; ++j)
-            a[j] = q[j] = 0;
+        for (int j = 0; j < 2 * H; ++j)
+            s[j] = 0;
 #pragma unroll 2
-        for (int k = 0; k < p.n; ++k) {
+        for (int r = 0; r < p.n; ++r) {
             Pair g[H], h[H], sg = 0, sb = 0;
-            chunk_to_pairs<T>(gmine[k * kThreads], g);
-            const float2 w = smine[k * shop];
+            chunk_to_pairs<T>(gmine[r * kThreads], g);
+            const float2 f = smine[r * p.stride];
             if constexpr (CK) {
                 uint32_t words[V / 4];
-                code_words<V>(cmine + k * kThreads * V, words);
+                code_words<V>(cmine + r * kThreads * V, words);
                 codes_to_pairs<H>(words, h);
             } else {
-                chunk_to_pairs<T>(xmine[k * kThreads], h);
+                chunk_to_pairs<T>(xmine[r * kThreads], h);
 #pragma unroll
                 for (int j = 0; j < H; ++j)
                     h[j] = mul2(add2(h[j], neg[j]), rstd[j]);
             }
-            const Pair w2 = twice(w.x), ws = twice(CK ? w.x * w.y : w.x);
+            const Pair w2 = twice(f.x), ws = twice(CK ? f.x * f.y : f.x);
 #pragma unroll
             for (int j = 0; j < H; ++j) {
                 const Pair gh = mul2(g[j], h[j]);
-                a[j] = fma2(g[j], w2, a[j]);
-                q[j] = fma2(gh, ws, q[j]);
+                s[j] = fma2(g[j], w2, s[j]);
+                s[H + j] = fma2(gh, ws, s[H + j]);
                 sg = j ? add2(sg, gh) : gh;
                 sb = j ? add2(sb, g[j]) : g[j];
             }
             if (part_g) {
                 const float2 x = halves(sg), y = halves(sb);
-                Pair *to = acc + threadIdx.x + k * kThreads;
-                *to = add2(*to, pair(CK ? (x.x + x.y) * w.y : x.x + x.y, y.x + y.y));
+                Pair *to = acc + threadIdx.x + r * kThreads;
+                *to = add2(*to, pair(CK ? (x.x + x.y) * f.y : x.x + x.y, y.x + y.y));
             }
         }
         if (P.gx) {
-#pragma unroll
-            for (int j = 0; j < H; ++j) {
-                over_rows(a[j]);
-                over_rows(q[j]);
-            }
-            if (p.lane < (1 << p.lpr_log))
-#pragma unroll
-                for (int j = 0; j < H; ++j) {
-                    const float2 x = halves(a[j]), y = halves(q[j]);
-                    part[threadIdx.x / 32][p.sub * V + 2 * j] = make_float2(x.x, y.x);
-                    part[threadIdx.x / 32][p.sub * V + 2 * j + 1] = make_float2(x.y, y.y);
-                }
+            put_row_sums<H, LPR_LOG>(s, part[threadIdx.x / 32], p.lpr_log, p.lane, p.sub);
             __syncthreads();
-            const int col = threadIdx.x;
-            float2 sum = make_float2(0.0f, 0.0f);
-            if (col < t.tw) {
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    sum.x += part[w][col].x;
-                    sum.y += part[w][col].y;
-                }
-                own[turn][col] = sum;
-            }
-            if (t.split > 1) {
-                // `own` alternates: a block writes one half while others may read the other,
-                // and passes the next barrier only after its reads of this one
-                cg::cluster_group cluster = cg::this_cluster();
-                cluster.sync();
-                if (col < t.tw) {
+            {   // eight threads a position, one a warp's sums
+                const int col = threadIdx.x / 8, g = threadIdx.x % 8;
+                float2 sum = make_float2(sum8(part[g][col]), sum8(part[g][kTW + col]));
+                if (t.split > 1) {
+                    // `own` alternates: a block writes one half while others may read the
+                    // other, and passes the next barrier only after its reads of this one
+                    cg::cluster_group cluster = cg::this_cluster();
+                    if (g == 0)
+                        own[turn][col] = sum;
+                    cluster.sync();
                     sum = make_float2(0.0f, 0.0f);
-                    for (int r = 0; r < t.split; ++r) {
-                        const float2 o = *cluster.map_shared_rank(&own[turn][col], r);
-                        sum.x += o.x;
-                        sum.y += o.y;
-                    }
+                    if (g < t.split)
+                        sum = *cluster.map_shared_rank(&own[turn][col], g);
+                    sum = make_float2(sum8(sum.x), sum8(sum.y));
                 }
+                if (g == 0)
+                    stat[col] = make_float2(-sum.x * t.inv_c, -sum.y * t.inv_c);
             }
-            if (col < t.tw)
-                stat[col] = make_float2(-sum.x * t.inv_c, -sum.y * t.inv_c);
             __syncthreads();
             // grad_x = rstd gamma gy - rstd A - v rstd S
             Pair rA[H], rS[H];
 #pragma unroll
             for (int j = 0; j < H; ++j) {
-                const float2 u = stat[p.sub * V + 2 * j], w = stat[p.sub * V + 2 * j + 1];
-                rA[j] = mul2(pair(u.x, w.x), rstd[j]);
-                rS[j] = mul2(pair(u.y, w.y), rstd[j]);
+                const float2 u = stat[p.sub * V + 2 * j], v = stat[p.sub * V + 2 * j + 1];
+                rA[j] = mul2(pair(u.x, v.x), rstd[j]);
+                rS[j] = mul2(pair(u.y, v.y), rstd[j]);
             }
             T *out = static_cast<T *>(P.gx) + base + p.row * P.L + p.sub * V;
             const int64_t hop = p.stride * P.L;
 #pragma unroll 2
-            for (int k = 0; k < p.n; ++k) {
+            for (int r = 0; r < p.n; ++r) {
                 Pair g[H], h[H];
-                chunk_to_pairs<T>(gmine[k * kThreads], g);
-                const float2 w = smine[k * shop];
-                const Pair w2 = twice(w.x);
+                chunk_to_pairs<T>(gmine[r * kThreads], g);
+                const float2 f = smine[r * p.stride];
+                const Pair w2 = twice(f.x);
                 if constexpr (CK) {
                     uint32_t words[V / 4];
-                    code_words<V>(cmine + k * kThreads * V, words);
+                    code_words<V>(cmine + r * kThreads * V, words);
                     codes_to_pairs<H>(words, h);
-                    const Pair step = twice(w.y);
+                    const Pair st = twice(f.y);
 #pragma unroll
                     for (int j = 0; j < H; ++j)
-                        h[j] = mul2(h[j], step);
+                        h[j] = mul2(h[j], st);
                 } else {
-                    chunk_to_pairs<T>(xmine[k * kThreads], h);
+                    chunk_to_pairs<T>(xmine[r * kThreads], h);
 #pragma unroll
                     for (int j = 0; j < H; ++j)
                         h[j] = mul2(add2(h[j], neg[j]), rstd[j]);
@@ -670,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 5) norm_grad_tile_kernel(const NormG
                     g[j] = fma2(h[j], rS[j], fma2(mul2(g[j], w2), rstd[j], rA[j]));
                 const uint4 u = pairs_to_chunk<T>(g);
                 if constexpr (!VEC)
-                    tile4[threadIdx.x + k * kThreads] = u;
+                    tile4[threadIdx.x + r * kThreads] = u;
                 else if (in)
                     *reinterpret_cast<uint4 *>(out) = u;
                 out += hop;
@@ -680,27 +743,461 @@ __global__ void __launch_bounds__(kThreads, 5) norm_grad_tile_kernel(const NormG
                 store_rows<T, V>(gtile, static_cast<T *>(P.gx) + base, P.L, left, nrow, t, p);
             }
         }
-        __syncwarp();   // the next tile's copies overwrite what the warp has read
-        turn ^= 1;
-        b += t.walk_b;
-        lt += t.walk_l;
-        if (lt >= tiles) {
-            lt -= tiles;
-            ++b;
-        }
+        __syncwarp();   // the next tile's values and steps overwrite what the warp has read
     }
     if (part_g) {
         float *out = part_g + (int64_t)cluster_at * 2 * P.C + c0;
-        for (int k = 0; k < p.warp_n; ++k) {
-            Pair v = k < p.n ? acc[threadIdx.x + k * kThreads] : 0;
+        for (int r = 0; r < p.warp_n; ++r) {
+            Pair v = r < p.n ? acc[threadIdx.x + r * kThreads] : 0;
             for (int o = 1; o < (1 << p.lpr_log); o <<= 1)
                 v = add2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-            const int i = p.row + k * p.stride;
-            if (k < p.n && p.sub == 0) {
+            const int i = p.row + r * p.stride;
+            if (r < p.n && p.sub == 0) {
                 const float2 f = halves(v);
                 out[i] = f.x;
                 out[P.C + i] = f.y;
             }
+        }
+    }
+    if (t.split > 1)
+        cg::this_cluster().sync();   // another block may still read this one's `own`
+}
+
+// ---------------------------------------------------------------- aligned rows
+//
+// Where rows are aligned for 16-byte chunks nothing is staged: a block walks the channels of
+// a tile of 64 positions (fp32: 32; 128 bytes of a row) twice, and the second walk finds the
+// tile in the L1 or the L2.  That leaves the shared memory to the L1, needs no copies, and
+// lets 24 to 32 warps an SM hide the latencies.
+
+constexpr int kStreamTW = 64;
+constexpr int kRows = 4;   // rows whose loads a thread has in flight
+
+template <class T, bool CK, int LPR_LOG>
+__global__ void __launch_bounds__(kThreads, 4) norm_stream_kernel(const NormProblem P,
+                                                                  const Tiling t) {
+    constexpr int V = Vec<T>::V, H = Vec<T>::H;
+    __shared__ __align__(8) float part[kWarps][2 * kStreamTW], part_k[kWarps][kStreamTW], count[kWarps];
+    __shared__ Moments own[kStreamTW];         // of the block's rows (cluster)
+    __shared__ float2 stat[kStreamTW];         // (-mean, rstd)
+    const int rank = t.split > 1 ? blockIdx.x % t.split : 0;
+    const Walk w(t, t.split > 1 ? blockIdx.x / t.split : blockIdx.x);
+    const int c0 = rank * t.slice;
+    const int nrow = min(t.slice, (int)P.C - c0);   // may be 0 or less in the last blocks
+    const Place<LPR_LOG> p(t, nrow);
+    const int64_t l0 = (int64_t)w.lt << t.tw_log, left = P.L - l0;
+    const int64_t base = (w.b * P.C + c0) * P.L + l0;
+    const bool in = p.sub * V < left;
+    // lanes past the end of the row, and of the slice, read the first values of b, for nothing
+    const T *safe = static_cast<const T *>(P.x) + w.b * P.C * P.L;
+    const T *x0 = in && p.n > 0 ? static_cast<const T *>(P.x) + base + p.row * P.L + p.sub * V : safe;
+    const int64_t hop = p.stride * P.L, x_hop = in ? hop : 0;
+    if (p.lane == 0) {
+        const int first = (int)threadIdx.x >> p.lpr_log, rows = 32 >> p.lpr_log;
+        int n = 0;                             // rows of the warp
+        for (int i = first; i < nrow; i += p.stride)
+            n += min(rows, nrow - i);
+        count[threadIdx.x / 32] = (float)n;
+    }
+    auto chunk = [](const T *at) { return __ldg(reinterpret_cast<const uint4 *>(at)); };
+    // k: the mean of the first rows of the warp's first lane of each position
+    Pair f[H], k[H], s[2 * H];
+    const int first = min(p.n, kFirstRows);
+#pragma unroll
+    for (int j = 0; j < H; ++j)
+        k[j] = 0;
+#pragma unroll
+    for (int r = 0; r < kFirstRows; ++r)
+        if (r < first) {
+            chunk_to_pairs<T>(chunk(x0 + r * x_hop), f);
+#pragma unroll
+            for (int j = 0; j < H; ++j)
+                k[j] = add2(k[j], f[j]);
+        }
+    const Pair over = twice(first > 0 ? -1.0f / (float)first : 0.0f);
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+        k[j] = __shfl_sync(0xFFFFFFFFu, mul2(k[j], over), p.sub);   // minus k
+        s[j] = s[H + j] = 0;
+    }
+    auto add_row = [&](const uint4 &u) {
+        chunk_to_pairs<T>(u, f);
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            const Pair d = add2(f[j], k[j]);
+            s[j] = add2(s[j], d);
+            s[H + j] = fma2(d, d, s[H + j]);
+        }
+    };
+    const T *x = x0;
+    int r = 0;
+    for (; r + kRows <= p.n; r += kRows) {
+        uint4 u[kRows];
+#pragma unroll
+        for (int q = 0; q < kRows; ++q, x += x_hop)
+            u[q] = chunk(x);
+#pragma unroll
+        for (int q = 0; q < kRows; ++q)
+            add_row(u[q]);
+    }
+    for (; r < p.n; ++r, x += x_hop)
+        add_row(chunk(x));
+    put_row_sums<H, LPR_LOG, kStreamTW>(s, part[threadIdx.x / 32], p.lpr_log, p.lane, p.sub);
+    if (p.lane < (1 << p.lpr_log))
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            const float2 u = halves(k[j]);
+            part_k[threadIdx.x / 32][p.sub * V + 2 * j] = -u.x;
+            part_k[threadIdx.x / 32][p.sub * V + 2 * j + 1] = -u.y;
+        }
+    __syncthreads();
+    // eight threads a position, one a warp's sums
+    for (int c = threadIdx.x / 8; c < t.tw; c += kThreads / 8) {
+        const int g = threadIdx.x % 8;
+        const Moments m = join8(Moments{part_k[g][c], part[g][c], part[g][kStreamTW + c]}, count[g]);
+        if (g == 0)
+            own[c] = m;
+    }
+    if (t.split > 1)
+        cg::this_cluster().sync();
+    else
+        __syncthreads();
+    for (int c = threadIdx.x / 8; c < t.tw; c += kThreads / 8) {
+        const int g = threadIdx.x % 8;
+        Moments m = own[c];
+        if (t.split > 1) {
+            static_assert(kMaxSplit == 8, "a thread for each block");
+            if (g < t.split)
+                m = *cg::this_cluster().map_shared_rank(&own[c], g);
+            m = join8(m, g < t.split ? (float)max(0, min(t.slice, (int)P.C - g * t.slice)) : 0.0f);
+        }
+        const float off = m.s1 * t.inv_c, var = fmaxf(m.s2 * t.inv_c - off * off, 0.0f);
+        const float rstd = 1.0f / sqrtf((m.s2 == m.s2 ? var : m.s2) + P.eps);   // fmaxf drops NaN
+        if (g == 0) {
+            stat[c] = make_float2(-(m.k + off), rstd);
+            if (rank == 0 && c < left) {
+                if (P.mean)
+                    P.mean[w.b * P.L + l0 + c] = m.k + off;
+                if (P.rstd)
+                    P.rstd[w.b * P.L + l0 + c] = rstd;
+            }
+        }
+    }
+    __syncthreads();
+    Pair rstd[H];
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+        const float2 u = stat[p.sub * V + 2 * j], v = stat[p.sub * V + 2 * j + 1];
+        k[j] = pair(u.x, v.x);
+        rstd[j] = pair(u.y, v.y);
+    }
+    const int64_t nb = ck_blocks(P.L);
+    const int lanes = min(kCkBlock / V, 1 << p.lpr_log);   // lanes of a block of 32 values
+    const T *gamma = P.gamma ? static_cast<const T *>(P.gamma) + c0 + p.row : nullptr;
+    const T *beta = P.beta ? static_cast<const T *>(P.beta) + c0 + p.row : nullptr;
+    T *y = static_cast<T *>(P.y) + base + p.row * P.L + p.sub * V;
+    int8_t *codes = P.codes + base + p.row * P.L + p.sub * V;
+    uint8_t *scale = P.scales + (w.b * P.C + c0 + p.row) * nb + (l0 + p.sub * V) / kCkBlock;
+    const int64_t scale_hop = p.stride * nb;
+    auto put_row = [&](const uint4 &u, int at, bool row) {
+        Pair v[H];
+        chunk_to_pairs<T>(u, v);
+        const Pair g = twice(gamma && row ? ld_f32(gamma + at * p.stride) : 1.0f);
+        const Pair be = twice(beta && row ? ld_f32(beta + at * p.stride) : 0.0f);
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            v[j] = mul2(add2(v[j], k[j]), rstd[j]);
+            f[j] = fma2(v[j], g, be);
+        }
+        const uint4 o = pairs_to_chunk<T>(f);
+        if (row && in)
+            *reinterpret_cast<uint4 *>(y) = o;
+        y += hop;
+        if constexpr (CK) {
+            float top = 0.0f;
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                const float2 a = halves(v[j]);
+                top = max_abs(max_abs(top, a.x), a.y);
+            }
+            uint32_t bits = row && in ? ck_abs_bits(top) : 0u;
+            if constexpr (LPR_LOG >= 0) {
+#pragma unroll
+                for (int o2 = 1; o2 < kCkBlock / V; o2 <<= 1)
+                    bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o2));
+            } else {
+                for (int o2 = 1; o2 < lanes; o2 <<= 1)
+                    bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o2));
+            }
+            const uint32_t e = ck_scale(bits, ck_top<float>());
+            uint32_t q[V / 4];
+            code_pairs<H>(v, ck_inverse(e), q);
+            if (row && in) {
+                put_code_words<V>(codes, q);
+                if ((p.sub & (lanes - 1)) == 0)
+                    *scale = (uint8_t)e;
+            }
+            codes += hop;
+            scale += scale_hop;
+        }
+    };
+    x = x0;
+    r = 0;
+    const int full = CK ? __shfl_sync(0xFFFFFFFFu, p.n, 31) : p.n;   // the warp's smallest
+    for (; r + kRows <= full; r += kRows) {
+        uint4 u[kRows];
+#pragma unroll
+        for (int q = 0; q < kRows; ++q, x += x_hop)
+            u[q] = chunk(x);
+#pragma unroll
+        for (int q = 0; q < kRows; ++q)
+            put_row(u[q], r + q, true);
+    }
+    // CK: whole warps walk together, for the block maximum's shuffles
+    for (; r < (CK ? p.warp_n : p.n); ++r, x += x_hop) {
+        const bool row = r < p.n;
+        put_row(chunk(row ? x : safe), r, row);
+    }
+    if (t.split > 1)
+        cg::this_cluster().sync();   // another block may still read this one's `own`
+}
+
+// A cluster of t.split blocks walks tiles cluster, cluster + n, ...; the sums of grad_y v
+// and grad_y over the walk stay in shared memory, a row of a warp's lanes each, and go to the
+// cluster's rows of `part_g` [clusters][2][C] at the end: a fixed order, no atomics.
+template <class T, bool CK, int LPR_LOG>
+__global__ void __launch_bounds__(kThreads, 3) norm_grad_stream_kernel(const NormGrad P,
+                                                                       const Tiling t,
+                                                                       float *part_g) {
+    constexpr int V = Vec<T>::V, H = Vec<T>::H;
+    extern __shared__ uint4 tile4[];
+    __shared__ __align__(8) float part[kWarps][2 * kStreamTW];
+    __shared__ float2 own[2][kStreamTW];
+    __shared__ float2 stat[kStreamTW];         // (-A, -S)
+    const int rank = t.split > 1 ? blockIdx.x % t.split : 0;
+    const unsigned cluster_at = t.split > 1 ? blockIdx.x / t.split : blockIdx.x;
+    const int c0 = rank * t.slice;
+    const int nrow = min(t.slice, (int)P.C - c0);
+    const Place<LPR_LOG> p(t, nrow);
+    Pair *acc = reinterpret_cast<Pair *>(tile4);               // [slice]: sums of a row
+    float *gam = reinterpret_cast<float *>(acc + t.slice);     // [slice]
+    const int64_t nb = ck_blocks(P.L);
+    for (int i = threadIdx.x; i < nrow; i += kThreads) {
+        acc[i] = 0;
+        gam[i] = P.gamma ? ld_f32(static_cast<const T *>(P.gamma) + c0 + i) : 1.0f;
+    }
+    __syncthreads();
+    const int64_t hop = p.stride * P.L, scale_hop = p.stride * nb;
+    const int full = __shfl_sync(0xFFFFFFFFu, p.n, 31);        // the warp's smallest n
+    int turn = 0;
+    for (Walk w(t, cluster_at); w.b < P.B; w.step(t), turn ^= 1) {
+        const int64_t l0 = (int64_t)w.lt << t.tw_log, left = P.L - l0;
+        const int64_t base = (w.b * P.C + c0) * P.L + l0;
+        const bool in = p.sub * V < left;
+        // lanes past the end of the row, and of the slice, read the tile's first chunk
+        const int64_t safe = w.b * P.C * P.L;
+        const int64_t mine = in && p.n > 0 ? base + p.row * P.L + p.sub * V : safe;
+        const int64_t v_hop = in ? hop : 0, e_hop = in ? scale_hop : 0;
+        const T *g0 = static_cast<const T *>(P.gy) + mine;
+        const T *x0 = static_cast<const T *>(P.x) + (CK ? 0 : mine);
+        const int8_t *c0p = P.codes + (CK ? mine : 0);
+        const uint8_t *e0 = P.scales;
+        if (CK)
+            e0 += in && p.n > 0 ? (w.b * P.C + c0 + p.row) * nb + (l0 + p.sub * V) / kCkBlock
+                                : w.b * P.C * nb;
+        Pair rstd[H], neg[H];                  // neg: minus the mean
+        {
+            const float *rs = P.rstd + w.b * P.L + (in ? l0 + p.sub * V : 0);
+            const float *me = CK ? nullptr : P.mean + w.b * P.L + (in ? l0 + p.sub * V : 0);
+#pragma unroll
+            for (int j = 0; j < H; j += 2) {
+                const float4 u = __ldg(reinterpret_cast<const float4 *>(rs) + j / 2);
+                rstd[j] = in ? pair(u.x, u.y) : 0;
+                rstd[j + 1] = in ? pair(u.z, u.w) : 0;
+                neg[j] = neg[j + 1] = 0;
+                if constexpr (!CK) {
+                    const float4 v = __ldg(reinterpret_cast<const float4 *>(me) + j / 2);
+                    neg[j] = pair(-v.x, -v.y);
+                    neg[j + 1] = pair(-v.z, -v.w);
+                }
+            }
+        }
+        // kRows rows' loads, then their use: a walk of this lane's rows
+        struct Row {
+            uint4 g, x;                        // CK: x.x, x.y the codes, x.w the step byte
+        };
+        auto fetch = [&](int r) {
+            Row u;
+            u.g = __ldg(reinterpret_cast<const uint4 *>(g0 + r * v_hop));
+            if constexpr (CK) {
+                uint32_t q[V / 4];
+                code_words<V>(c0p + r * v_hop, q);
+                u.x.x = q[0];
+                u.x.y = q[V / 4 - 1];
+                u.x.w = __ldg(e0 + r * e_hop);
+            } else {
+                u.x = __ldg(reinterpret_cast<const uint4 *>(x0 + r * v_hop));
+            }
+            return u;
+        };
+        auto open = [&](const Row &u, Pair (&g)[H], Pair (&h)[H]) {
+            chunk_to_pairs<T>(u.g, g);
+            if constexpr (CK) {
+                uint32_t q[V / 4];
+                q[0] = u.x.x;
+                q[V / 4 - 1] = u.x.y;
+                codes_to_pairs<H>(q, h);
+            } else {
+                chunk_to_pairs<T>(u.x, h);
+#pragma unroll
+                for (int j = 0; j < H; ++j)
+                    h[j] = mul2(add2(h[j], neg[j]), rstd[j]);
+            }
+        };
+        // the checkpoint's v is h step, with one step a chunk: gamma gy v = (gy h) (gamma step)
+        Pair s[2 * H];
+#pragma unroll
+        for (int j = 0; j < 2 * H; ++j)
+            s[j] = 0;
+        auto add_row = [&](const Row &u, float w1) {   // returns (sum gy v, sum gy)
+            Pair g[H], h[H], sg = 0, sb = 0;
+            open(u, g, h);
+            const float st = CK ? ck_step(u.x.w) : 1.0f;
+            const Pair w2 = twice(w1), ws = twice(CK ? w1 * st : w1);
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                const Pair gh = mul2(g[j], h[j]);
+                s[j] = fma2(g[j], w2, s[j]);
+                s[H + j] = fma2(gh, ws, s[H + j]);
+                sg = j ? add2(sg, gh) : gh;
+                sb = j ? add2(sb, g[j]) : g[j];
+            }
+            const float2 a = halves(sg), b = halves(sb);
+            return in ? pair(CK ? (a.x + a.y) * st : a.x + a.y, b.x + b.y) : Pair(0);
+        };
+        int r = 0;
+        for (; r + kRows <= full; r += kRows) {
+            Row u[kRows];
+            Pair a[kRows];
+#pragma unroll
+            for (int q = 0; q < kRows; ++q)
+                u[q] = fetch(r + q);
+#pragma unroll
+            for (int q = 0; q < kRows; ++q)
+                a[q] = add_row(u[q], gam[p.row + (r + q) * p.stride]);
+            if (part_g) {
+                if constexpr (LPR_LOG == 3) {
+                    // four rows over eight lanes: two halving exchanges and one sum
+                    const bool u4 = p.sub & 4, u2 = p.sub & 2;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        a[q] = add2(u4 ? a[q + 2] : a[q],
+                                    __shfl_xor_sync(0xFFFFFFFFu, u4 ? a[q] : a[q + 2], 4));
+                    a[0] = add2(u2 ? a[1] : a[0], __shfl_xor_sync(0xFFFFFFFFu, u2 ? a[0] : a[1], 2));
+                    a[0] = add2(a[0], __shfl_xor_sync(0xFFFFFFFFu, a[0], 1));
+                    if (!(p.sub & 1)) {
+                        Pair *to = acc + p.row + (r + (p.sub >> 1)) * p.stride;
+                        *to = add2(*to, a[0]);
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < kRows; ++q) {
+                        for (int o = 1; o < (1 << p.lpr_log); o <<= 1)
+                            a[q] = add2(a[q], __shfl_xor_sync(0xFFFFFFFFu, a[q], o));
+                        if (p.sub == 0) {
+                            Pair *to = acc + p.row + (r + q) * p.stride;
+                            *to = add2(*to, a[q]);
+                        }
+                    }
+                }
+            }
+        }
+        for (; r < p.warp_n; ++r) {
+            const bool row = r < p.n;
+            Pair a = row ? add_row(fetch(r), gam[p.row + r * p.stride]) : 0;
+            if (part_g) {
+                for (int o = 1; o < (1 << p.lpr_log); o <<= 1)
+                    a = add2(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+                if (row && p.sub == 0) {
+                    Pair *to = acc + p.row + r * p.stride;
+                    *to = add2(*to, a);
+                }
+            }
+        }
+        if (!P.gx)
+            continue;
+        put_row_sums<H, LPR_LOG, kStreamTW>(s, part[threadIdx.x / 32], p.lpr_log, p.lane, p.sub);
+        __syncthreads();
+        for (int c = threadIdx.x / 8; c < t.tw; c += kThreads / 8) {
+            const int q = threadIdx.x % 8;     // eight threads a position, one a warp's sums
+            const float2 sum = make_float2(sum8(part[q][c]), sum8(part[q][kStreamTW + c]));
+            if (q == 0)
+                own[turn][c] = sum;
+            if (t.split == 1 && q == 0)
+                stat[c] = make_float2(-sum.x * t.inv_c, -sum.y * t.inv_c);
+        }
+        if (t.split > 1) {
+            // `own` alternates: a block writes one half while others may read the other, and
+            // passes the next barrier only after its reads of this one
+            cg::cluster_group cluster = cg::this_cluster();
+            cluster.sync();
+            for (int c = threadIdx.x / 8; c < t.tw; c += kThreads / 8) {
+                const int q = threadIdx.x % 8;
+                float2 sum = make_float2(0.0f, 0.0f);
+                if (q < t.split)
+                    sum = *cluster.map_shared_rank(&own[turn][c], q);
+                sum = make_float2(sum8(sum.x), sum8(sum.y));
+                if (q == 0)
+                    stat[c] = make_float2(-sum.x * t.inv_c, -sum.y * t.inv_c);
+            }
+        }
+        __syncthreads();
+        // grad_x = rstd gamma gy - rstd A - v rstd S
+        Pair rA[H], rS[H];
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            const float2 u = stat[p.sub * V + 2 * j], v = stat[p.sub * V + 2 * j + 1];
+            rA[j] = mul2(pair(u.x, v.x), rstd[j]);
+            rS[j] = mul2(pair(u.y, v.y), rstd[j]);
+        }
+        T *out = static_cast<T *>(P.gx) + base + p.row * P.L + p.sub * V;
+        auto put_row = [&](const Row &u, int at) {
+            Pair g[H], h[H];
+            open(u, g, h);
+            const Pair w2 = twice(gam[p.row + at * p.stride]);
+            if constexpr (CK) {
+                const Pair st = twice(ck_step(u.x.w));
+#pragma unroll
+                for (int j = 0; j < H; ++j)
+                    h[j] = mul2(h[j], st);
+            }
+#pragma unroll
+            for (int j = 0; j < H; ++j)
+                g[j] = fma2(h[j], rS[j], fma2(mul2(g[j], w2), rstd[j], rA[j]));
+            if (in)
+                *reinterpret_cast<uint4 *>(out) = pairs_to_chunk<T>(g);
+            out += hop;
+        };
+        r = 0;
+        for (; r + kRows <= p.n; r += kRows) {
+            Row u[kRows];
+#pragma unroll
+            for (int q = 0; q < kRows; ++q)
+                u[q] = fetch(r + q);
+#pragma unroll
+            for (int q = 0; q < kRows; ++q)
+                put_row(u[q], r + q);
+        }
+        for (; r < p.n; ++r)
+            put_row(fetch(r), r);
+    }
+    if (part_g) {
+        __syncthreads();
+        float *out = part_g + (int64_t)cluster_at * 2 * P.C + c0;
+        for (int i = threadIdx.x; i < nrow; i += kThreads) {
+            const float2 f = halves(acc[i]);
+            out[i] = f.x;
+            out[P.C + i] = f.y;
         }
     }
     if (t.split > 1)
@@ -1120,12 +1617,12 @@ bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 // cluster, and so are the channels of a tile where there are too few tiles for the SMs (at
 // least as many channels a block as its threads have rows).
 template <class Bytes>
-bool make_tiling(int64_t B, int64_t C, int64_t L, int size, Bytes row_bytes, Tiling *t) {
+bool make_tiling(int64_t B, int64_t C, int64_t L, int size, int most, Bytes row_bytes, Tiling *t) {
     const int V = 16 / size;
     if (L < 2)
         return false;
     t->tw = V;
-    while (t->tw < kRowBytes / size && t->tw < L)
+    while (t->tw < most && t->tw < L)
         t->tw *= 2;
     t->tw_log = __builtin_ctz(t->tw);
     t->lpr_log = __builtin_ctz(t->tw / V);
@@ -1136,21 +1633,29 @@ bool make_tiling(int64_t B, int64_t C, int64_t L, int size, Bytes row_bytes, Til
     auto slice = [&](int split) { return ((C + split - 1) / split + rows - 1) / rows * rows; };
     auto shared = [&](int split) { return slice(split) * row_bytes(t->tw); };
     t->split = 1;
-    while (t->split < kMaxSplit && shared(t->split) > 70 * 1024)
+    while (t->split < kMaxSplit && shared(t->split) > 69 * 1024)
         t->split *= 2;
-    if (shared(t->split) > 200 * 1024)
+    if (shared(t->split) > 200 * 1024 || (most == kTW && slice(t->split) > kMaxSlice))
         return false;
     while (t->split < kMaxSplit && t->total * t->split < sm_count_or(148) &&
            slice(t->split) >= 2 * rows)
         t->split *= 2;
     t->slice = (int)slice(t->split);
-    return t->total * t->split < (1LL << 31);
+    return true;
 }
 
 // Blocks of a tile kernel that one SM holds.
 int blocks_per_sm(size_t shared) {
-    const int n = (int)((227 * 1024) / (shared + 5 * 1024));   // 5 KB: static and reserved
-    return n < 1 ? 1 : n > 5 ? 5 : n;   // 5: registers
+    const int n = (int)((227 * 1024) / (shared + 6 * 1024));   // 6 KB: static and reserved
+    return n < 1 ? 1 : n > 3 ? 3 : n;   // 3: registers
+}
+
+// Clusters of a launch, `room` at most, and the step of their walks.
+int64_t plan_walk(Tiling *t, int64_t room) {
+    const int64_t n = t->total < room ? t->total : room;
+    t->walk_b = (int)(n / t->tiles);
+    t->walk_l = (int)(n % t->tiles);
+    return n;
 }
 
 template <class... A>
@@ -1204,16 +1709,25 @@ cudaError_t norm(const NormProblem &P, cudaStream_t s) {
     }
     Tiling t;
     const bool vec = base && P.L % V == 0;
-    auto row_bytes = [&](int tw) { return tw * (int)sizeof(T) + (!vec && P.codes ? tw : 0); };
-    if (make_tiling(P.B, P.C, P.L, sizeof(T), row_bytes, &t)) {
-        const unsigned grid = (unsigned)(t.total * t.split);
+    auto row_bytes = [&](int tw) { return norm_row_bytes<T>(tw, vec, P.codes != nullptr); };
+    constexpr int WIDE = 128 / (int)sizeof(T);
+    if (vec && make_tiling(P.B, P.C, P.L, sizeof(T), WIDE, [](int) { return 0; }, &t)) {
+        const bool full = t.tw == WIDE;
+        auto kernel = P.codes ? (full ? norm_stream_kernel<T, true, 3> : norm_stream_kernel<T, true, -1>)
+                              : (full ? norm_stream_kernel<T, false, 3>
+                                      : norm_stream_kernel<T, false, -1>);
+        return launch_cluster(kernel, (unsigned)(t.total * t.split), (unsigned)t.split, 0, s, P, t);
+    }
+    if (make_tiling(P.B, P.C, P.L, sizeof(T), kTW, row_bytes, &t)) {
         const size_t shared = (size_t)t.slice * row_bytes(t.tw);
-        const bool full = vec && t.lpr_log == 3;
+        const unsigned grid = (unsigned)(plan_walk(&t, (int64_t)sm_count_or(148) * blocks_per_sm(shared) / t.split) * t.split);
+        constexpr int FULL = sizeof(T) == 2 ? 2 : 3;   // log2 of the lanes of a full row
+        const bool full = vec && t.tw == kTW;
         auto kernel =
-            P.codes ? (full ? norm_tile_kernel<T, true, true, 3>
+            P.codes ? (full ? norm_tile_kernel<T, true, true, FULL>
                             : vec ? norm_tile_kernel<T, true, true, -1>
                                   : norm_tile_kernel<T, false, true, -1>)
-                    : (full ? norm_tile_kernel<T, true, false, 3>
+                    : (full ? norm_tile_kernel<T, true, false, FULL>
                             : vec ? norm_tile_kernel<T, true, false, -1>
                                   : norm_tile_kernel<T, false, false, -1>);
         return launch_cluster(kernel, grid, (unsigned)t.split, shared, s, P, t);
@@ -1254,16 +1768,22 @@ GradPlan grad_plan(const NormGrad &P) {
             return g;
         }
     }
-    auto row_bytes = [&](int tw) { return grad_row_bytes<T>(tw, P.from_codes); };
-    if (make_tiling(P.B, P.C, P.L, sizeof(T), row_bytes, &g.t)) {
-        g.kind = 1;
-        g.vec = base && P.L % V == 0;
-        g.shared = (size_t)g.t.slice * row_bytes(g.t.tw);
-        const int64_t room = (int64_t)sms * blocks_per_sm(g.shared) / g.t.split;
-        g.rows = g.t.total < room ? g.t.total : room;
+    g.vec = base && P.L % V == 0;
+    if (g.vec && make_tiling(P.B, P.C, P.L, sizeof(T), 128 / (int)sizeof(T),
+                             [](int) { return (int)(sizeof(float) * 3); }, &g.t)) {
+        g.kind = 4;
+        g.shared = (size_t)g.t.slice * sizeof(float) * 3;
+        const int64_t room = (int64_t)sms * 3 / g.t.split;
+        g.rows = plan_walk(&g.t, room);
         g.blocks = g.rows * g.t.split;
-        g.t.walk_b = (int)(g.rows / g.t.tiles);
-        g.t.walk_l = (int)(g.rows % g.t.tiles);
+        return g;
+    }
+    auto row_bytes = [&](int tw) { return grad_row_bytes<T>(tw, g.vec, P.from_codes); };
+    if (make_tiling(P.B, P.C, P.L, sizeof(T), kTW, row_bytes, &g.t)) {
+        g.kind = 1;
+        g.shared = (size_t)g.t.slice * row_bytes(g.t.tw);
+        g.rows = plan_walk(&g.t, (int64_t)sms * blocks_per_sm(g.shared) / g.t.split);
+        g.blocks = g.rows * g.t.split;
         return g;
     }
     const int TL = lanes_along(P.L);
@@ -1275,10 +1795,14 @@ GradPlan grad_plan(const NormGrad &P) {
 template <class T, bool CK>
 cudaError_t run_norm_grad(const NormGrad &P, const GradPlan &g, float *part, cudaStream_t s) {
     const unsigned grid = (unsigned)g.blocks;
+    if (g.kind == 4)
+        return launch_cluster(g.t.tw == 128 / (int)sizeof(T) ? norm_grad_stream_kernel<T, CK, 3>
+                                                             : norm_grad_stream_kernel<T, CK, -1>,
+                              grid, (unsigned)g.t.split, g.shared, s, P, g.t, part);
     if (g.kind == 1)
         return launch_cluster(!g.vec              ? norm_grad_tile_kernel<T, false, CK, -1>
-                              : g.t.lpr_log == 3 ? norm_grad_tile_kernel<T, true, CK, 3>
-                                                 : norm_grad_tile_kernel<T, true, CK, -1>,
+                              : g.t.tw == kTW ? norm_grad_tile_kernel<T, true, CK, sizeof(T) == 2 ? 2 : 3>
+                                              : norm_grad_tile_kernel<T, true, CK, -1>,
                               grid, (unsigned)g.t.split, g.shared, s, P, g.t, part);
     if (g.kind >= 2) {
         auto kernel = g.kind == 2 ? (g.nv == 1   ? norm_grad_row_kernel<T, 32, 1, CK>
