@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormG
 // lets 24 to 32 warps an SM hide the latencies.
 
 constexpr int kStreamTW = 64;
-constexpr int kRows = 4;   // rows whose loads a thread has in flight
+constexpr int kRows = 4, kGradRows = 8;   // rows whose loads a thread has in flight
 
 template <class T, bool CK, int LPR_LOG>
 __global__ void __launch_bounds__(kThreads, 4) norm_stream_kernel(const NormProblem P,
@@ -966,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_stream_kernel(const NormProb
 // and grad_y over the walk stay in shared memory, a row of a warp's lanes each, and go to the
 // cluster's rows of `part_g` [clusters][2][C] at the end: a fixed order, no atomics.
 template <class T, bool CK, int LPR_LOG>
-__global__ void __launch_bounds__(kThreads, 3) norm_grad_stream_kernel(const NormGrad P,
+__global__ void __launch_bounds__(kThreads, 2) norm_grad_stream_kernel(const NormGrad P,
                                                                        const Tiling t,
                                                                        float *part_g) {
     constexpr int V = Vec<T>::V, H = Vec<T>::H;
@@ -1022,7 +1022,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_grad_stream_kernel(const Nor
                 }
             }
         }
-        // kRows rows' loads, then their use: a walk of this lane's rows
+        // kGradRows rows' loads, then their use: a walk of this lane's rows
         struct Row {
             uint4 g, x;                        // CK: x.x, x.y the codes, x.w the step byte
         };
@@ -1076,32 +1076,31 @@ __global__ void __launch_bounds__(kThreads, 3) norm_grad_stream_kernel(const Nor
             return in ? pair(CK ? (a.x + a.y) * st : a.x + a.y, b.x + b.y) : Pair(0);
         };
         int r = 0;
-        for (; r + kRows <= full; r += kRows) {
-            Row u[kRows];
-            Pair a[kRows];
+        for (; r + kGradRows <= full; r += kGradRows) {
+            Row u[kGradRows];
+            Pair a[kGradRows];
 #pragma unroll
-            for (int q = 0; q < kRows; ++q)
+            for (int q = 0; q < kGradRows; ++q)
                 u[q] = fetch(r + q);
 #pragma unroll
-            for (int q = 0; q < kRows; ++q)
+            for (int q = 0; q < kGradRows; ++q)
                 a[q] = add_row(u[q], gam[p.row + (r + q) * p.stride]);
             if (part_g) {
                 if constexpr (LPR_LOG == 3) {
-                    // four rows over eight lanes: two halving exchanges and one sum
-                    const bool u4 = p.sub & 4, u2 = p.sub & 2;
+                    // eight rows over eight lanes, by halving exchanges: lane sub has row sub
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        a[q] = add2(u4 ? a[q + 2] : a[q],
-                                    __shfl_xor_sync(0xFFFFFFFFu, u4 ? a[q] : a[q + 2], 4));
-                    a[0] = add2(u2 ? a[1] : a[0], __shfl_xor_sync(0xFFFFFFFFu, u2 ? a[0] : a[1], 2));
-                    a[0] = add2(a[0], __shfl_xor_sync(0xFFFFFFFFu, a[0], 1));
-                    if (!(p.sub & 1)) {
-                        Pair *to = acc + p.row + (r + (p.sub >> 1)) * p.stride;
-                        *to = add2(*to, a[0]);
+                    for (int m = 4; m >= 1; m >>= 1) {
+                        const bool upper = p.sub & m;
+#pragma unroll
+                        for (int q = 0; q < m; ++q)
+                            a[q] = add2(upper ? a[q + m] : a[q],
+                                        __shfl_xor_sync(0xFFFFFFFFu, upper ? a[q] : a[q + m], m));
                     }
+                    Pair *to = acc + p.row + (r + p.sub) * p.stride;
+                    *to = add2(*to, a[0]);
                 } else {
 #pragma unroll
-                    for (int q = 0; q < kRows; ++q) {
+                    for (int q = 0; q < kGradRows; ++q) {
                         for (int o = 1; o < (1 << p.lpr_log); o <<= 1)
                             a[q] = add2(a[q], __shfl_xor_sync(0xFFFFFFFFu, a[q], o));
                         if (p.sub == 0) {
@@ -1179,13 +1178,13 @@ __global__ void __launch_bounds__(kThreads, 3) norm_grad_stream_kernel(const Nor
             out += hop;
         };
         r = 0;
-        for (; r + kRows <= p.n; r += kRows) {
-            Row u[kRows];
+        for (; r + kGradRows <= p.n; r += kGradRows) {
+            Row u[kGradRows];
 #pragma unroll
-            for (int q = 0; q < kRows; ++q)
+            for (int q = 0; q < kGradRows; ++q)
                 u[q] = fetch(r + q);
 #pragma unroll
-            for (int q = 0; q < kRows; ++q)
+            for (int q = 0; q < kGradRows; ++q)
                 put_row(u[q], r + q);
         }
         for (; r < p.n; ++r)
@@ -1773,7 +1772,7 @@ GradPlan grad_plan(const NormGrad &P) {
                              [](int) { return (int)(sizeof(float) * 3); }, &g.t)) {
         g.kind = 4;
         g.shared = (size_t)g.t.slice * sizeof(float) * 3;
-        const int64_t room = (int64_t)sms * 3 / g.t.split;
+        const int64_t room = (int64_t)sms * 2 / g.t.split;
         g.rows = plan_walk(&g.t, room);
         g.blocks = g.rows * g.t.split;
         return g;
