@@ -1174,7 +1174,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_stream_kernel(const Nor
             for (int j = 0; j < H; ++j)
                 g[j] = fma2(h[j], rS[j], fma2(mul2(g[j], w2), rstd[j], rA[j]));
             if (in)
-                *reinterpret_cast<uint4 *>(out) = pairs_to_chunk<T>(g);
+                __stcs(reinterpret_cast<uint4 *>(out), pairs_to_chunk<T>(g));   // not to be kept
             out += hop;
         };
         r = 0;
