@@ -268,3 +268,80 @@ def test_far_and_bad_offsets_read_nothing_outside(K, og):
         a, b = got[n][1:].double(), clean[n].double()
         assert ((a - b).abs() <= 2 * R.half_step(gout.dtype) * b.abs()
                 + 1e-5 * b.abs().max()).all(), n
+
+
+@pytest.mark.parametrize("dt,C,L,K,mask", [("bf16", 3, 700, 3, False), ("f16", 2, 1200, 2, True),
+                                          ("f32", 3, 700, 3, True), ("bf16", 2, 5000, 5, True)])
+def test_many_taps_at_one_site(dt, C, L, K, mask):
+    """Every tap of a row samples near position 100, so thousands of equal contributions meet
+    at two sites; the oracle adds them in 64 bits.  Position and fraction are exact in the
+    type (offsets are whole multiples of 1/4 up to L in fp32, rounded by the type before)."""
+    T = TYPES[dt]
+    l = torch.arange(L)[:, None]
+    k = torch.arange(K)[None]
+    off = (100.25 - (l + k)).to(T).expand(2, C, L, K).contiguous()
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(2, C, L, generator=g).to(T)
+    w = torch.ones(C, 1, K).to(T)
+    gout = torch.ones(2, C, L + K - 1).to(T)[:, :, :L].contiguous()
+    m = torch.full((2, C, L, K), 0.5).to(T) if mask else None
+    args = (1, (0, K - 1), 1, C, C, True)
+    kept = dcn.dcn1d_checkpoint_pack(x.cuda())
+    dev = [None if t is None else t.cuda() for t in (off, m, w, gout)]
+    got = dcn.dcn1d_backward_checkpoint(kept, *dev, *args)
+    back = dcn.dcn1d_checkpoint_unpack(kept, dtype=T).cpu()
+    ref = oracle.backward(back, off, m, w, gout, *args)
+    for n, t in got.items():
+        assert norm_err(t.double().cpu().numpy(), ref[NAMES[n]]) <= TOL[dt], n
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dt", TYPES)
+def test_bad_gradients_reach_their_sites_only(dt, bad):
+    T = TYPES[dt]
+    C, L, K = 4, 200, 3
+    g = torch.Generator().manual_seed(8)
+    x = torch.randn(2, C, L, generator=g).to(T).cuda()
+    off = (0.5 * torch.randn(2, C, L, K, generator=g)).to(T).cuda()
+    w = (1 + torch.rand(C, 1, K, generator=g)).to(T).cuda()
+    gout = torch.randn(2, C, L, generator=g).to(T).cuda()
+    kept = dcn.dcn1d_checkpoint_pack(x)
+    args = (1, 1, 1, C, C, False)
+    clean = dcn.dcn1d_backward_checkpoint(kept, off, None, w, gout, *args)
+    gout[1, 2, 90] = bad
+    got = dcn.dcn1d_backward_checkpoint(kept, off, None, w, gout, *args)
+    hit = ~torch.isfinite(got["x"])
+    assert hit[1, 2, 88:93].any() and hit.sum() == hit[1, 2, 88:93].sum()
+    a, b = got["x"][~hit].double(), clean["x"][~hit].double()
+    assert ((a - b).abs() <= 2 * R.half_step(T) * b.abs() + 1e-5 * b.abs().max()).all()
+    touched = ~torch.isfinite(got["offsets"])
+    assert touched[1, 2, 90].any() and touched.sum() == touched[1, 2, 90].sum()
+
+
+@pytest.mark.parametrize("dt", TYPES)
+def test_gradients_of_very_different_size_in_one_row(dt):
+    """Output gradients from 1 down to 2^-9 in stretches of a row: the small ones' grad_x is
+    compared on its own.  Fixed point of unit M 2^-22 leaves them 13 bits and more of their
+    own largest, below half a step of bf16 (2^-8) and fp16 (2^-11)."""
+    T = TYPES[dt]
+    C, L, K = 3, 1024, 3
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(1, C, L, generator=g).to(T)
+    off = torch.zeros(1, C, L, K).to(T)
+    w = torch.ones(C, 1, K).to(T)
+    size = 2.0 ** -(torch.arange(L) // 128 * 9 // 7).double()
+    gout = (torch.randn(1, C, L, generator=g).double() * size).to(T)
+    args = (1, 1, 1, C, C, False)
+    kept = dcn.dcn1d_checkpoint_pack(x.cuda())
+    got = dcn.dcn1d_backward_checkpoint(kept, off.cuda(), None, w.cuda(), gout.cuda(), *args,
+                                        wanted=("x",))["x"].double().cpu()
+    ref = torch.from_numpy(oracle.backward(dcn.dcn1d_checkpoint_unpack(kept, dtype=T).cpu(), off,
+                                           None, w, gout, *args)["grad_x"])
+    M = gout.double().abs().amax()
+    # three contributions a site and its neighbours' zeros: six roundings to the unit
+    unit = M * (2.0 ** -22 if dt != "f32" else 2.0 ** -28)
+    fp32 = 4 * R.U * ref.abs().amax() if dt == "f32" else 0.0
+    room = R.half_step(T) * ref.abs() + 6 * unit + fp32
+    for at in range(0, L, 128):
+        part = slice(at + 2, at + 126)
+        assert ((got - ref)[:, :, part].abs() <= room[:, :, part]).all(), at
