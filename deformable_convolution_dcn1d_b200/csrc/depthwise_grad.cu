@@ -45,6 +45,7 @@ struct Args {
     int x_words, sum_words;              // 4-byte words of a row's x and of each sum's array
     int a_bits, b_bits;                  // A and B above (16-bit types: A = 22)
     bool wide;                           // offsets' gradients leave in 16-byte chunks
+    bool even;                           // 16-bit types: two positions' values are whole words
     int64_t rows, nb;
 };
 
@@ -59,9 +60,11 @@ int row_words(const Problem &P) {
     return words_of(P, P.dtype == DCN1D_F32 ? 4 : 2) + sums_of(P) * words_of(P, 4);
 }
 
-// Staging of a warp's 32 positions' gradients of offsets (and mask).
+constexpr int kGroup = 64;               // positions of a warp's step, two neighbours a lane
+
+// Staging of a group's gradients of offsets (and mask).
 int stage_bytes(const Problem &P) {
-    return 32 * P.K * (P.dtype == DCN1D_F32 ? 4 : 2) * (P.mask ? 2 : 1);
+    return kGroup * P.K * (P.dtype == DCN1D_F32 ? 4 : 2) * (P.mask ? 2 : 1);
 }
 
 constexpr float kRound = 12582912.0f;    // 1.5 * 2^23: adding it rounds to an integer
@@ -70,12 +73,12 @@ constexpr unsigned kRoundBits = 0x4B400000u;
 // 2^e as a float, -126 <= e <= 127.
 __device__ __forceinline__ float two_to(int e) { return __uint_as_float((unsigned)(e + 127) << 23); }
 
-// The `n` staged values of 32 positions (fewer at the row's end) to global memory.
+// The `n` staged values of a group (fewer at the row's end) to global memory.
 template <class T, int K>
 __device__ __forceinline__ void unstage(const T *from, T *to, int n, bool wide) {
-    constexpr int VE = 16 / (int)sizeof(T), CHUNKS = 32 * K / VE;
+    constexpr int VE = 16 / (int)sizeof(T), CHUNKS = kGroup * K / VE;
     const int lane = threadIdx.x & 31;
-    if (wide && n == 32 * K) {
+    if (wide && n == kGroup * K) {
 #pragma unroll
         for (int c = lane; c < (CHUNKS + 31) / 32 * 32; c += 32)
             if (c < CHUNKS)
@@ -130,8 +133,8 @@ __device__ __forceinline__ float bits_to_f32(uint32_t b) {
         return __uint_as_float(b << 16);
 }
 
-// Block of blockDim.x / 32 warps, wpr of them a row.
-template <class T, int K, bool MASK>
+// Block of blockDim.x / 32 warps, wpr of them a row.  ALL: every gradient is wanted.
+template <class T, int K, bool MASK, bool ALL>
 __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(const Args a) {
     constexpr bool TWO = sizeof(T) == 4;                   // two words a sum
     extern __shared__ uint4 raw4[];
@@ -147,13 +150,14 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
     const int64_t row = (int64_t)blockIdx.x * rpb + mine;
     const bool live = row < a.rows;
     const int L = P.L_in, Lo = P.L_out;
+    const bool want_x = ALL || G.x, want_off = ALL || G.off, want_mask = MASK && (ALL || G.mask);
     // site s stands for position s - 1
     const int words = a.x_words + (TWO ? 2 : 1) * a.sum_words;
     uint32_t *base = reinterpret_cast<uint32_t *>(raw4) + (size_t)mine * words;
     T *xs = reinterpret_cast<T *>(base) + lead<T>();
     int *hi = reinterpret_cast<int *>(base + a.x_words) + 3, *lo = hi + a.sum_words;   // lo: TWO
     T *stage = reinterpret_cast<T *>(reinterpret_cast<uint32_t *>(raw4) + (size_t)rpb * words) +
-               warp * 32 * K * (MASK ? 2 : 1);
+               warp * kGroup * K * (MASK ? 2 : 1);
     const int c = live ? (int)(row % P.C_in) : 0;
     const int64_t out0 = row * Lo;
     const T *gout = static_cast<const T *>(G.gout) + out0;
@@ -210,7 +214,7 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
 #pragma unroll
         for (int k = 0; k < K; ++k)
             w[k] = ld_f32(static_cast<const T *>(P.w) + c * K + k);
-        if (G.x) {
+        if (want_x) {
             const uint32_t tg = top_bits(gout, Lo, lane, lanes);
             const uint32_t tm = MASK ? top_bits(mask, (int64_t)Lo * K, lane, lanes) : 0u;
             const uint32_t wg = __reduce_max_sync(0xFFFFFFFFu, tg), wm = __reduce_max_sync(0xFFFFFFFFu, tm);
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
     float to_hi = 0.0f;                                    // 2^s
     int s = 0;
     bool fixed = true;
-    if (live && G.x) {
+    if (live && want_x) {
         uint32_t bg = 0, bm = 0;
         for (int i = 0; i < a.wpr; ++i) {
             bg = max(bg, tops[mine * a.wpr + i][0]);
@@ -255,120 +259,182 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
     T *goff = static_cast<T *>(G.off) + (G.off ? out0 * K : 0);
     T *gmask = static_cast<T *>(G.mask) + (G.mask ? out0 * K : 0);
     // All taps of the row.  FIXED: grad_x in fixed point, and whether a site came near the
-    // end of its range; again: grad_x alone, the rest has been written.
-    auto walk = [&](auto tag, bool again) {
-        constexpr bool FIXED = decltype(tag)::value;
-        uint32_t near_end = 0;
-        T o_next[K], m_next[K], g_next = from_f32<T>(0.0f);
-        auto fetch = [&](int l0) {
-            const int l = min(l0 + me, Lo - 1);
-            const T *po = off + l * K, *pm = mask + l * K;
+    // end of its range; AGAIN: grad_x alone, the rest has been written.
+    auto walk = [&](auto fixed_tag, auto again_tag) {
+        constexpr bool FIXED = decltype(fixed_tag)::value, AGAIN = decltype(again_tag)::value;
+        constexpr int W = TWO ? 2 * K : K;                 // words of two positions' offsets
+        uint32_t near_end = 0, o_next[W], m_next[MASK ? W : 1], g_next[TWO ? 2 : 1];
+        auto two = [&](const T *from, uint32_t *to, int l, int per) {
+            // `per` values of positions l and l + 1 (kept inside the row)
+            if (!TWO && a.even) {
+                const uint32_t *p = reinterpret_cast<const uint32_t *>(from + l * per);
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                o_next[k] = __ldg(po + k);
-                if (MASK)
-                    m_next[k] = __ldg(pm + k);
+                for (int k = 0; k < K; ++k)
+                    if (k < per)
+                        to[k] = __ldg(p + k);
+                return;
             }
-            g_next = __ldg(gout + l);
+            const int l1 = min(l + 1, Lo - 1);
+#pragma unroll
+            for (int k = 0; k < 2 * K; ++k)
+                if (k < 2 * per) {
+                    const T *p = k < per ? from + l * per + k : from + l1 * per + k - per;
+                    if constexpr (TWO)
+                        to[k] = __ldg(reinterpret_cast<const uint32_t *>(p));
+                    else if (k % 2 == 0)
+                        to[k / 2] = __ldg(reinterpret_cast<const unsigned short *>(p));
+                    else
+                        to[k / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(p)) << 16;
+                }
         };
-        int l0 = row_warp * 32;
+        // value i of those words
+        auto at = [](const uint32_t *w, int i) -> float {
+            if constexpr (TWO)
+                return __uint_as_float(w[i]);
+            else if constexpr (std::is_same<T, __half>::value)
+                return __half2float(__ushort_as_half((unsigned short)(i % 2 ? w[i / 2] >> 16 : w[i / 2])));
+            else
+                return __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+        };
+        auto fetch = [&](int l0) {
+            int l = l0 + 2 * me;
+            if (l >= Lo)                                   // an even position with two values
+                l = (Lo - 1) & ~1;
+            two(off, o_next, l, K);
+            if (MASK)
+                two(mask, m_next, l, K);
+            two(gout, g_next, l, 1);
+        };
+        int l0 = row_warp * kGroup;
         if (l0 < Lo)
             fetch(l0);
-        for (; l0 < Lo; l0 += lanes) {
-            float o[K], m[K];
+        for (; l0 < Lo; l0 += 2 * lanes) {
+            uint32_t o[W], m[MASK ? W : 1], gg[TWO ? 2 : 1];
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                o[k] = to_f32(o_next[k]);
-                m[k] = MASK ? to_f32(m_next[k]) : 1.0f;
+            for (int k = 0; k < W; ++k) {
+                o[k] = o_next[k];
+                if (MASK)
+                    m[k] = m_next[k];
             }
-            const float g = l0 + me < Lo ? to_f32(g_next) : 0.0f;   // lanes past the end add zeros
-            if (l0 + lanes < Lo)
-                fetch(l0 + lanes);
-            if (!again)
-                gb += g;
-            const float start = (float)(min(l0 + me, Lo - 1) * P.stride - P.padding);
-            const float first = start + from_start, last = start + to_end;
-            int found0[K], found1[K];
+            gg[0] = g_next[0];
+            if (TWO)
+                gg[TWO ? 1 : 0] = g_next[TWO ? 1 : 0];
+            if (l0 + 2 * lanes < Lo)
+                fetch(l0 + 2 * lanes);
+            const float start0 = (float)((l0 + 2 * me) * P.stride - P.padding);
+            float doff[2 * K], dmask[MASK ? 2 * K : 1];
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                const float raw = __fadd_rn(start + (float)(k * P.dilation), o[k]);
-                const float pos = fminf(fmaxf(raw, first), last);
-                // floor by one addition rounded down (sampler.cuh); positions too far for it
-                // give a site past the signal, like all that lie outside
-                const float t = __fadd_rd(pos, kFloorMagic);
-                const float f = __fsub_rn(pos, __fsub_rn(t, kFloorMagic));
-                const uint32_t site = min(__float_as_uint(t) - (kFloorMagicBits - 1u), (uint32_t)L + 1u);
-                const float dv = w[k] * g, mdv = MASK ? m[k] * dv : dv;
-                if (!again) {
-                    const float x0 = to_f32(xs[site]), x1 = to_f32(xs[site + 1]);
-                    const float slope = x1 - x0, v = fmaf(f, slope, x0);
-                    gw[k] = fmaf(MASK ? m[k] * g : g, v, gw[k]);
-                    if (G.off)   // no gradient where the clamp moved the tap
-                        stage[me * K + k] = from_f32<T>(pos == raw ? slope * mdv : 0.0f);
-                    if (MASK && G.mask)
-                        stage[32 * K + me * K + k] = from_f32<T>(v * dv);
-                }
-                if (G.x) {
-                    const float d = site <= (uint32_t)L ? mdv : 0.0f;   // far taps add zeros
-                    const float c1 = f * d, c0 = d - c1;
-                    if constexpr (FIXED) {
-                        const float h0 = fmaf(c0, to_hi, kRound), h1 = fmaf(c1, to_hi, kRound);
-                        found0[k] = atomicAdd(hi + site, (int)(__float_as_uint(h0) - kRoundBits));
-                        found1[k] = atomicAdd(hi + site + 1, (int)(__float_as_uint(h1) - kRoundBits));
-                        if constexpr (TWO) {
-                            const float r0 = fmaf(c0, to_hi, kRound - h0), r1 = fmaf(c1, to_hi, kRound - h1);
-                            atomicAdd(lo + site, (int)(__float_as_uint(fmaf(r0, to_lo, kRound)) - kRoundBits));
-                            atomicAdd(lo + site + 1,
-                                      (int)(__float_as_uint(fmaf(r1, to_lo, kRound)) - kRoundBits));
+            for (int u = 0; u < 2; ++u) {
+                const float g = l0 + 2 * me + u < Lo ? at(gg, u) : 0.0f;   // past the end: zeros
+                if (!AGAIN)
+                    gb += g;
+                const float start = u ? start0 + (float)P.stride : start0;
+                const float first = start + from_start, last = start + to_end;
+                int found[2 * K];
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const float raw = __fadd_rn(start + (float)(k * P.dilation), at(o, u * K + k));
+                    const float pos = fminf(fmaxf(raw, first), last);
+                    // floor by one addition rounded down (sampler.cuh); positions too far for
+                    // it give a site past the signal, like all that lie outside
+                    const float t = __fadd_rd(pos, kFloorMagic);
+                    const float f = __fsub_rn(pos, __fsub_rn(t, kFloorMagic));
+                    const uint32_t site =
+                        min(__float_as_uint(t) - (kFloorMagicBits - 1u), (uint32_t)L + 1u);
+                    const float mk = MASK ? at(m, u * K + k) : 1.0f;
+                    const float dv = w[k] * g, mdv = MASK ? mk * dv : dv;
+                    if (!AGAIN) {
+                        const float x0 = to_f32(xs[site]), x1 = to_f32(xs[site + 1]);
+                        const float slope = x1 - x0, v = fmaf(f, slope, x0);
+                        gw[k] = fmaf(MASK ? mk * g : g, v, gw[k]);
+                        // no gradient where the clamp moved the tap
+                        doff[u * K + k] = pos == raw ? slope * mdv : 0.0f;
+                        if (MASK)
+                            dmask[u * K + k] = v * dv;
+                    }
+                    if (want_x) {
+                        const float d = site <= (uint32_t)L ? mdv : 0.0f;   // far taps add zeros
+                        const float c1 = f * d, c0 = d - c1;
+                        if constexpr (FIXED) {
+                            const float h0 = fmaf(c0, to_hi, kRound), h1 = fmaf(c1, to_hi, kRound);
+                            found[2 * k] = atomicAdd(hi + site, (int)(__float_as_uint(h0) - kRoundBits));
+                            found[2 * k + 1] =
+                                atomicAdd(hi + site + 1, (int)(__float_as_uint(h1) - kRoundBits));
+                            if constexpr (TWO) {
+                                const float r0 = fmaf(c0, to_hi, kRound - h0),
+                                            r1 = fmaf(c1, to_hi, kRound - h1);
+                                atomicAdd(lo + site,
+                                          (int)(__float_as_uint(fmaf(r0, to_lo, kRound)) - kRoundBits));
+                                atomicAdd(lo + site + 1,
+                                          (int)(__float_as_uint(fmaf(r1, to_lo, kRound)) - kRoundBits));
+                            }
+                        } else {
+                            atomicAdd(reinterpret_cast<float *>(hi) + site, c0);
+                            atomicAdd(reinterpret_cast<float *>(hi) + site + 1, c1);
                         }
-                    } else {
-                        atomicAdd(reinterpret_cast<float *>(hi) + site, c0);
-                        atomicAdd(reinterpret_cast<float *>(hi) + site + 1, c1);
+                    }
+                }
+                if constexpr (FIXED && !TWO) {
+                    if (want_x) {
+#pragma unroll
+                        for (int k = 0; k < 2 * K; ++k)    // bit 31: 2^30 or more, either sign
+                            near_end |= (uint32_t)found[k] + 0x40000000u;
                     }
                 }
             }
-            if constexpr (FIXED && !TWO) {
-                if (G.x) {
-#pragma unroll
-                    for (int k = 0; k < K; ++k)            // the top two bits differ: 2^30 or more
-                        near_end |= (found0[k] ^ (found0[k] << 1)) | (found1[k] ^ (found1[k] << 1));
-                }
-            }
-            if (again)
+            if constexpr (AGAIN)
                 continue;
-            const int n = min(32, Lo - l0) * K;
+            const int n = min(kGroup, Lo - l0) * K;
+            auto put = [&](T *to, const float (&d)[2 * K]) {
+                if constexpr (TWO) {
+#pragma unroll
+                    for (int k = 0; k < 2 * K; ++k)
+                        to[2 * K * me + k] = from_f32<T>(d[k]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        const T q[2] = {from_f32<T>(d[2 * k]), from_f32<T>(d[2 * k + 1])};
+                        reinterpret_cast<uint32_t *>(to)[K * me + k] = *reinterpret_cast<const uint32_t *>(q);
+                    }
+                }
+            };
+            if (want_off)
+                put(stage, doff);
+            if constexpr (MASK)
+                if (want_mask)
+                    put(stage + kGroup * K, dmask);
             __syncwarp();
-            if (G.off)
+            if (want_off)
                 unstage<T, K>(stage, goff + l0 * K, n, a.wide);
-            if (MASK && G.mask)
-                unstage<T, K>(stage + 32 * K, gmask + l0 * K, n, a.wide);
+            if (want_mask)
+                unstage<T, K>(stage + kGroup * K, gmask + l0 * K, n, a.wide);
             __syncwarp();
         }
         return near_end >> 31;
     };
     if (live) {
         if (fixed) {
-            if (walk(std::true_type(), false))
+            if (walk(std::true_type(), std::false_type()))
                 over[mine * a.wpr] = 1;
         } else {
-            walk(std::false_type(), false);
+            walk(std::false_type(), std::false_type());
         }
     }
     if constexpr (!TWO) {
         __syncthreads();
-        const bool redo = live && G.x && fixed && over[mine * a.wpr];
+        const bool redo = live && want_x && fixed && over[mine * a.wpr];
         if (__syncthreads_or(redo)) {
             if (redo)
                 clear();
             __syncthreads();
             if (redo) {
                 fixed = false;
-                walk(std::false_type(), true);
+                walk(std::false_type(), std::true_type());
             }
         }
     }
     __syncthreads();
-    if (live && G.x) {
+    if (live && want_x) {
         T *gx = static_cast<T *>(G.x) + row * L;
         const float from_hi = two_to(-s), from_lo = two_to(-a.b_bits);
         auto value = [&](int i) {
@@ -453,6 +519,8 @@ cudaError_t run(const CheckpointConv &q, void *ws, cudaStream_t s, int *launches
     const int es = P.dtype == DCN1D_F32 ? 4 : 2;
     a.wide = (int64_t)P.L_out * K % (16 / es) == 0 &&
              ((reinterpret_cast<uintptr_t>(G.off) | reinterpret_cast<uintptr_t>(G.mask)) & 15) == 0;
+    a.even = P.L_out % 2 == 0 && ((reinterpret_cast<uintptr_t>(P.off) | reinterpret_cast<uintptr_t>(P.mask) |
+                                   reinterpret_cast<uintptr_t>(G.gout)) & 3) == 0;
     // a warp for each 64 positions, up to the block; then as many rows as make a block of
     // 8 warps
     const int longest = P.L_out > P.L_in ? P.L_out : P.L_in;
@@ -463,7 +531,11 @@ cudaError_t run(const CheckpointConv &q, void *ws, cudaStream_t s, int *launches
     while (rpb > 1 && block_bytes(P, a.wpr, rpb) > 48 * 1024)
         rpb /= 2;
     const size_t shared = block_bytes(P, a.wpr, rpb);
-    auto kernel = P.mask ? depthwise_grad_kernel<T, K, true> : depthwise_grad_kernel<T, K, false>;
+    const bool all = G.x && G.off && (!P.mask || G.mask);
+    auto kernel = P.mask ? (all ? depthwise_grad_kernel<T, K, true, true>
+                                : depthwise_grad_kernel<T, K, true, false>)
+                         : (all ? depthwise_grad_kernel<T, K, false, true>
+                                : depthwise_grad_kernel<T, K, false, false>);
     const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kernel), (int)shared);
     if (e != cudaSuccess)
         return e;
