@@ -644,38 +644,45 @@ def _scales_shape(B, C, L):
     return (B, blocks, 1) if L == 1 else (B, C, blocks)
 
 
-def _empty_checkpoint(shape, dev):
-    if len(shape) != 3:
+def _empty_checkpoint(x):
+    if x.ndim != 3:
         raise ValueError("a checkpoint is of a [B, C, L] tensor")
-    return Checkpoint8(torch.empty(shape, dtype=torch.int8, device=dev),
-                       torch.empty(_scales_shape(*shape), dtype=torch.uint8, device=dev))
+    return Checkpoint8(torch.empty_like(x, dtype=torch.int8),
+                       x.new_empty(_scales_shape(*x.shape), dtype=torch.uint8))
 
 
 _PACK = struct.Struct("@Pii4q").pack_into       # a dcn1d_tensor
 _DESC_BYTES = ctypes.sizeof(Dcn1dTensor)
-_NO_SIZES = tuple((0,) * (4 - n) for n in range(5))
+_CODE_OF = _DTYPES.get
+_buffer_of = ctypes.c_char.from_buffer
 
 
 def _pack(tensors):
     """(keep, addresses): descriptors of contiguous tensors (None -> None) in one block of
-    memory that lives as long as ``keep``.  A third of the cost of a ctypes structure each,
-    which is what a small call spends most of its time on."""
+    memory that lives as long as ``keep``.  A quarter of the cost of a ctypes structure each;
+    marshalling is most of what a small call takes."""
     keep = bytearray(_DESC_BYTES * len(tensors))
-    at = ctypes.addressof(ctypes.c_char.from_buffer(keep))
+    at = ctypes.addressof(_buffer_of(keep))
     out = []
     off = 0
     for t in tensors:
         if t is None:
             out.append(None)
         else:
-            shape = t.shape
             if not t.is_contiguous():
                 raise ValueError("tensors must be contiguous")
+            shape = t.shape
             n = len(shape)
-            if n > 4:
+            code = _CODE_OF(t.dtype, _BAD_DTYPE)
+            if n == 3:
+                x, y, z = shape
+                _PACK(keep, off, t.data_ptr(), code, 3, x, y, z, 0)
+            elif n == 1:
+                _PACK(keep, off, t.data_ptr(), code, 1, shape[0], 0, 0, 0)
+            elif n <= 4:
+                _PACK(keep, off, t.data_ptr(), code, n, *shape, *(0,) * (4 - n))
+            else:
                 raise ValueError("at most 4 dimensions")
-            _PACK(keep, off, t.data_ptr(), _DTYPES.get(t.dtype, _BAD_DTYPE), n, *shape,
-                  *_NO_SIZES[n])
             out.append(at + off)
         off += _DESC_BYTES
     return keep, out
@@ -683,17 +690,33 @@ def _pack(tensors):
 
 def _device_index(tensors):
     """The CUDA device that all tensors are on."""
-    dev = -1
+    dev = None
     for t in tensors:
         if t is not None:
             d = t.get_device()
-            if d < 0:
-                raise ValueError("every tensor must be on a CUDA device")
-            if dev < 0:
+            if d != dev:
+                if d < 0:
+                    raise ValueError("every tensor must be on a CUDA device")
+                if dev is not None:
+                    raise ValueError("every tensor must be on the same CUDA device")
                 dev = d
-            elif d != dev:
-                raise ValueError("every tensor must be on the same CUDA device")
     return dev
+
+
+class _Here:
+    """The context of a call on the current device and stream."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Here()
+# the current stream's handle without a Stream object around it, where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _on(dev, stream):
@@ -704,9 +727,8 @@ def _on(dev, stream):
         if stream.device.index != dev:
             raise ValueError(f"stream is on {stream.device}, the tensors are on cuda:{dev}")
         return torch.cuda.stream(stream), stream.cuda_stream
-    ctx = (contextlib.nullcontext() if torch.cuda.current_device() == dev
-           else torch.cuda.device(dev))
-    return ctx, torch.cuda.current_stream(dev).cuda_stream
+    ctx = _HERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+    return ctx, _raw_stream(dev)
 
 
 def _check_status(st, where):
@@ -722,7 +744,7 @@ def _workspace(need, workspace, like, where):
     if need == 0:
         return None, None, 0
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        workspace = like.new_empty(need, dtype=torch.uint8)
     elif (workspace.device != like.device or workspace.dtype != torch.uint8
           or workspace.numel() < need or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be a uint8 tensor of >= {need} bytes on {like.device}")
@@ -749,12 +771,12 @@ def dcn1d_layer_norm_forward(x, gamma=None, beta=None, eps=1e-5, stats=True, che
         mean = rstd = kept = None
         if stats and x.ndim == 3:
             size = (x.shape[0], x.shape[2])
-            mean = torch.empty(size, dtype=torch.float32, device=x.device)
-            rstd = torch.empty(size, dtype=torch.float32, device=x.device)
+            mean = x.new_empty(size, dtype=torch.float32)
+            rstd = torch.empty_like(mean)
         if codes is not None:
             kept = Checkpoint8(codes, scales)
         elif checkpoint:
-            kept = _empty_checkpoint(x.shape, x.device)
+            kept = _empty_checkpoint(x)
             codes, scales = kept
         keep, d = _pack((x, gamma, beta, out, mean, rstd, codes, scales))
         st = lib.dcn1d_layer_norm_forward(d[0], d[1], d[2], eps, d[3], d[4], d[5], d[6], d[7],
@@ -791,8 +813,12 @@ def dcn1d_layer_norm_backward(x, gamma, mean, rstd, grad_y, wanted=NORM_GRADS, g
         shape = grad_y.shape
         for n in res:
             if res[n] is None:
-                res[n] = torch.empty(shape if n == "x" else shape[1:2], dtype=grad_y.dtype,
-                                     device=grad_y.device)
+                if n == "x":
+                    res[n] = torch.empty_like(grad_y)
+                elif gamma is not None:
+                    res[n] = torch.empty_like(gamma)
+                else:
+                    res[n] = grad_y.new_empty(shape[1:2])
         keep, d = _pack((x, gamma, mean, rstd, codes, scales, grad_y, res.get("x"),
                          res.get("gamma"), res.get("beta")))
         key = (dev, shape, grad_y.dtype, x is None, d[8] is None and d[9] is None)
@@ -816,7 +842,7 @@ def dcn1d_checkpoint_pack(x, out=None, stream=None):
     lib = load()
     ctx, raw = _on(dev, stream)
     with ctx:
-        kept = Checkpoint8(*out) if out is not None else _empty_checkpoint(x.shape, x.device)
+        kept = Checkpoint8(*out) if out is not None else _empty_checkpoint(x)
         keep, d = _pack((x, *kept))
         st = lib.dcn1d_checkpoint_pack(*d, raw)
     _check_status(st, "dcn1d_checkpoint_pack")
