@@ -1580,6 +1580,8 @@ template <class T>
 __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float *part, int64_t n,
                                                                int64_t C, T *ggamma, T *gbeta) {
     __shared__ float sums[32][33];
+    // launched while the gradient's kernel still runs: wait for its partial sums
+    cudaGridDependencySynchronize();
     const int lane = threadIdx.x & 31, group = threadIdx.x / 32;
     const int64_t i = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.0f;
@@ -1831,8 +1833,20 @@ cudaError_t norm_grad(const NormGrad &P, void *ws, cudaStream_t s, int *launches
         ++*launches;
     }
     if (weights) {
-        norm_weight_grad_kernel<T><<<(unsigned)((2 * P.C + 31) / 32), 1024, 0, s>>>(
-            part, g.rows, P.C, static_cast<T *>(P.ggamma), static_cast<T *>(P.gbeta));
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)((2 * P.C + 31) / 32));
+        cfg.blockDim = dim3(1024);
+        cfg.stream = s;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_weight_grad_kernel<T>,
+                                                 static_cast<const float *>(part), g.rows, P.C,
+                                                 static_cast<T *>(P.ggamma), static_cast<T *>(P.gbeta));
+        if (e != cudaSuccess)
+            return e;
         ++*launches;
     }
     return cudaGetLastError();

@@ -233,6 +233,28 @@ def test_empty_inputs():
         assert (got["gamma"] == 0).all() and (got["beta"] == 0).all()
 
 
+def test_more_than_2_31_elements():
+    # 2^31 + 2^22 values: offsets pass 32 bits; checked at both ends
+    B, C, L = 1026, 512, 4096
+    x = torch.empty(B, C, L, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator("cuda").manual_seed(4)
+    x[0].normal_(generator=g)
+    x[1:] = x[0]
+    x[-1] *= -1
+    y, mean, rstd, kept = dcn.dcn1d_layer_norm_forward(x, checkpoint=True)
+    assert torch.equal(y[0], y[-2]) and torch.equal(y[0], -y[-1])
+    assert torch.equal(kept.codes[0], -kept.codes[-1])
+    assert torch.equal(kept.scales[0], kept.scales[-1])
+    back = dcn.dcn1d_checkpoint_unpack(kept, dtype=torch.bfloat16)
+    assert torch.equal(back[0], -back[-1])
+    got = dcn.dcn1d_layer_norm_backward(kept, None, None, rstd, x, wanted=("x",))["x"]
+    assert torch.equal(got[0], -got[-1]) and torch.equal(got[0], got[-2])
+    v = R.values(kept.codes[:1], kept.scales[:1])
+    ref = R.norm_grads(v, rstd[:1].double(), None, x[:1])
+    bound = R.grad_bounds(v, torch.zeros_like(v), rstd[:1].double(), None, x[:1], x.dtype)
+    within(got[:1], ref["x"], bound["x"], "x")
+
+
 def test_streams_and_a_replayed_graph():
     x, gy, gamma, beta = make((2, 128, 200), torch.bfloat16, 16)
     want = dcn.dcn1d_layer_norm_forward(x, gamma, beta, checkpoint=True)
