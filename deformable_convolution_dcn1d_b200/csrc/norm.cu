@@ -7,15 +7,18 @@
 //   grad_gamma[c] = sum_{b,l} grad_y v,   grad_beta[c] = sum_{b,l} grad_y
 //
 // A few flops a value: the bytes bound all of it.  The normalised axis is strided by L in
-// memory, so the tile kernels keep a tile of 32 positions x all channels in shared memory
-// and read every value once: 64 bytes (fp32: 128) of each channel's row, less when L is
-// shorter.  A thread owns 16-byte chunks, V = 16 / sizeof(T) positions of every
-// (kThreads / lanes of a row)-th channel, copies them itself, asynchronously, and needs no
-// barrier to use them; while it works on one tile the next one's copies are under way.
-// Sums over channels stay in registers until one exchange between lanes, warps and, where
-// the channels are split over the blocks of a cluster, distributed shared memory.  Each
-// warp takes its sums about a k near its mean, s1 = sum (x - k) and s2 = sum (x - k)^2, and
-// groups of n_i values are joined about a common k by
+// memory, so a block takes a tile of neighbouring positions x all channels (or, where they
+// are many or tiles few, a cluster's block a slice of the channels): lanes of a warp lie
+// along the positions, 16-byte chunks of V = 16 / sizeof(T) of them, and over channels.
+// Sums over channels stay in registers, two fp32 values an instruction, until one exchange
+// between lanes, warps and, in a cluster, distributed shared memory.
+//  * Rows aligned for 16-byte accesses: the stream kernels below.
+//  * Other rows: tiles staged in shared memory.
+//  * Single tokens (L == 1): rows of C values in registers.
+//  * Channels past what a cluster holds, unaligned single tokens: the simple kernels.
+//
+// The forward takes its sums about a k near the mean, s1 = sum (x - k) and s2 = sum (x -
+// k)^2, a k for each warp, and joins groups of n_i values about a common k by
 //   s1 = sum_i s1_i + n_i d_i,  s2 = sum_i s2_i + 2 d_i s1_i + n_i d_i^2,  d_i = k_i - k:
 // one exchange instead of one for the mean and one for the variance, and no difference of
 // large squares however far the mean is from zero (s1 carries what rounding k lost).
@@ -65,30 +68,16 @@ __device__ __forceinline__ uint4 f32_to_chunk(const float (&f)[Vec<T>::V]) {
     return u;
 }
 
-// BYTES (4, 8 or 16) from global to shared memory without a register; zeros when !in (the
-// source is then not read).
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void *dst, const void *src, bool in) {
-    const int n = in ? BYTES : 0;
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
-                     "r"(n)
-                     : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src),
-                     "n"(BYTES), "r"(n)
-                     : "memory");
+// Four bytes from global to shared memory without a register; zeros when !in (the source is
+// then not read).
+__device__ __forceinline__ void copy_async4(void *dst, const void *src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(in ? 4 : 0)
+                 : "memory");
 }
 
 __device__ __forceinline__ void copies_landed() {
     asm volatile("cp.async.wait_all;" ::: "memory");
-}
-
-__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-// All but the last group issued.
-__device__ __forceinline__ void earlier_copies_landed() {
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
 }
 
 // Where a thread stands in its block's tile.  Chunk k of a tile is row k / lpr, part k % lpr;
@@ -109,51 +98,38 @@ struct Place {
     }
 };
 
-// A block's rows of `E` values (T, or codes), tw a row: global rows start at src + row * L.
-// VEC: each thread copies its own chunks (rows are aligned for it and hold whole chunks).
-// Otherwise lanes run along the values, each warp over the rows of its threads' chunks, and
-// the warp meets afterwards; 4-byte values are copied asynchronously too.
-template <class E, int V, bool VEC, class P>
+// A block's rows of `E` values (T, or codes), tw a row, to shared memory: global rows start
+// at src + row * L.  Lanes run along the values, each warp over the rows of its threads'
+// chunks, and the warp meets afterwards; 4-byte values are copied asynchronously.
+template <class E, int V>
 __device__ __forceinline__ void load_rows(E *tile, const E *src, int64_t L, int64_t left, int nrow,
-                                          const Tiling &t, const P &p) {
-    if constexpr (VEC) {
-        const bool in = p.sub * V < left;
-        const E *from = in ? src + p.row * L + p.sub * V : src;
-        const int64_t step = in ? p.stride * L : 0;
-        E *to = tile + threadIdx.x * V;
-#pragma unroll 4
-        for (int j = 0; j < p.n; ++j) {
-            copy_async<V * (int)sizeof(E)>(to + j * kThreads * V, from, in);
-            from += step;
-        }
-    } else {
-        const int row0 = (int)(threadIdx.x & ~31u) >> p.lpr_log;   // the warp's first row
+                                          const Tiling &t, const Place<-1> &p) {
+    const int row0 = (int)(threadIdx.x & ~31u) >> p.lpr_log;   // the warp's first row
 #pragma unroll 2
-        for (int j = 0; j < p.warp_n; ++j) {
-            E *to = tile + ((threadIdx.x & ~31u) + j * kThreads) * V;
-            const E *from = src + (row0 + j * p.stride) * L;
-            E v[V];
+    for (int j = 0; j < p.warp_n; ++j) {
+        E *to = tile + ((threadIdx.x & ~31u) + j * kThreads) * V;
+        const E *from = src + (row0 + j * p.stride) * L;
+        E v[V];
 #pragma unroll
-            for (int q = 0; q < V; ++q) {
-                const int e = p.lane + 32 * q, r = e >> t.tw_log, col = e & (t.tw - 1);
-                const bool in = row0 + j * p.stride + r < nrow && col < left;
-                if constexpr (sizeof(E) == 4)
-                    copy_async<4>(to + e, in ? from + r * L + col : src, in);
-                else
-                    v[q] = in ? from[r * L + col] : E(0.0f);
-            }
-            if constexpr (sizeof(E) < 4)
-#pragma unroll
-                for (int q = 0; q < V; ++q)
-                    to[p.lane + 32 * q] = v[q];
+        for (int q = 0; q < V; ++q) {
+            const int e = p.lane + 32 * q, r = e >> t.tw_log, col = e & (t.tw - 1);
+            const bool in = row0 + j * p.stride + r < nrow && col < left;
+            if constexpr (sizeof(E) == 4)
+                copy_async4(to + e, in ? from + r * L + col : src, in);
+            else
+                v[q] = in ? from[r * L + col] : E(0.0f);
         }
+        if constexpr (sizeof(E) < 4)
+#pragma unroll
+            for (int q = 0; q < V; ++q)
+                to[p.lane + 32 * q] = v[q];
     }
 }
 
 // The same rows back to global memory, values along the lanes.
-template <class E, int V, class P>
+template <class E, int V>
 __device__ __forceinline__ void store_rows(const E *tile, E *dst, int64_t L, int64_t left, int nrow,
-                                           const Tiling &t, const P &p) {
+                                           const Tiling &t, const Place<-1> &p) {
     const int row0 = (int)(threadIdx.x & ~31u) >> p.lpr_log;
 #pragma unroll 2
     for (int j = 0; j < p.warp_n; ++j) {
@@ -305,61 +281,58 @@ struct Walk {
 
 constexpr int kFirstRows = 4;   // rows of a lane that give its warp's k
 
-template <class T, bool VEC, bool CK, int LPR_LOG>
+// Rows of a warp of a block's `nrow`, as a float.
+template <class P>
+__device__ __forceinline__ float warp_rows(const P &p, int nrow) {
+    const int rows = 32 >> p.lpr_log;
+    int n = 0;
+    for (int i = (int)(threadIdx.x & ~31u) >> p.lpr_log; i < nrow; i += p.stride)
+        n += min(rows, nrow - i);
+    return (float)n;
+}
+
+// (-mean, rstd) of C values from their sums, NaN kept (fmaxf drops it).
+__device__ __forceinline__ float2 finish(const Moments &m, const Tiling &t, float eps) {
+    const float off = m.s1 * t.inv_c, var = fmaxf(m.s2 * t.inv_c - off * off, 0.0f);
+    return make_float2(-(m.k + off), 1.0f / sqrtf((m.s2 == m.s2 ? var : m.s2) + eps));
+}
+
+// ---------------------------------------------------------------- unaligned rows
+//
+// A tile of 32 positions (fewer when L is shorter) x the block's channels in shared memory,
+// read and written with the lanes along the values, worked on in 16-byte chunks.
+
+template <class T, bool CK>
 __global__ void __launch_bounds__(kThreads, 3) norm_tile_kernel(const NormProblem P,
                                                                 const Tiling t) {
     constexpr int V = Vec<T>::V, H = Vec<T>::H;
-    extern __shared__ uint4 tile4[];           // VEC: two tiles; else one, then its codes
-    __shared__ __align__(8) float part[kWarps][2 * kTW], part_k[kWarps][kTW], count[kWarps];
+    extern __shared__ uint4 tile4[];           // the tile, then its codes
+    __shared__ __align__(8) float part[kWarps][2 * kTW];
+    __shared__ float part_k[kWarps][kTW], count[kWarps];
     __shared__ Moments own[2][kTW];            // of the block's rows (cluster)
     __shared__ float2 stat[kTW];               // (-mean, rstd)
     const int rank = t.split > 1 ? blockIdx.x % t.split : 0;
-    Walk w(t, t.split > 1 ? blockIdx.x / t.split : blockIdx.x), ahead = w;
+    Walk w(t, t.split > 1 ? blockIdx.x / t.split : blockIdx.x);
     const int c0 = rank * t.slice;
     const int nrow = min(t.slice, (int)P.C - c0);   // may be 0 or less in the last blocks
-    const Place<LPR_LOG> p(t, nrow);
-    const int chunks = t.slice << p.lpr_log;   // of a tile
-    int8_t *ctile = reinterpret_cast<int8_t *>(tile4 + chunks);
+    const Place<-1> p(t, nrow);
+    T *tile = reinterpret_cast<T *>(tile4);
+    int8_t *ctile = reinterpret_cast<int8_t *>(tile4 + (t.slice << p.lpr_log));
+    uint4 *mine = tile4 + threadIdx.x;
     const int64_t nb = ck_blocks(P.L);
-    const int lanes = min(kCkBlock / V, 1 << p.lpr_log);   // lanes of a block of 32 values
     const T *gamma = P.gamma ? static_cast<const T *>(P.gamma) + c0 + p.row : nullptr;
     const T *beta = P.beta ? static_cast<const T *>(P.beta) + c0 + p.row : nullptr;
-    const int64_t hop = p.stride * P.L, scale_hop = p.stride * nb;
-    auto load = [&](const Walk &at, int stage) {
-        const int64_t l0 = (int64_t)at.lt << t.tw_log;
-        load_rows<T, V, VEC>(reinterpret_cast<T *>(tile4 + stage * chunks),
-                             static_cast<const T *>(P.x) + (at.b * P.C + c0) * P.L + l0, P.L,
-                             P.L - l0, nrow, t, p);
-    };
-    if (p.lane == 0) {
-        const int first = (int)threadIdx.x >> p.lpr_log, rows = 32 >> p.lpr_log;
-        int n = 0;                             // rows of the warp
-        for (int i = first; i < nrow; i += p.stride)
-            n += min(rows, nrow - i);
-        count[threadIdx.x / 32] = (float)n;
-    }
-    if constexpr (VEC) {
-        load(w, 0);
-        copies_issued();
-    }
+    const float rows = warp_rows(p, nrow);
+    if (p.lane == 0)
+        count[threadIdx.x / 32] = rows;
     int turn = 0;
     for (; w.b < P.B; w.step(t), turn ^= 1) {
         const int64_t l0 = (int64_t)w.lt << t.tw_log;
         const int64_t left = P.L - l0;         // positions of this tile (tw or more: all)
         const int64_t base = (w.b * P.C + c0) * P.L + l0;
-        const int stage = VEC ? turn : 0;
-        if constexpr (VEC) {
-            ahead.step(t);
-            if (ahead.b < P.B)
-                load(ahead, stage ^ 1);
-            copies_issued();
-            earlier_copies_landed();
-        } else {
-            load(w, 0);
-            copies_landed();
-            __syncwarp();
-        }
-        uint4 *mine = tile4 + stage * chunks + threadIdx.x;
+        load_rows<T, V>(tile, static_cast<const T *>(P.x) + base, P.L, left, nrow, t, p);
+        copies_landed();
+        __syncwarp();
         // k: the mean of the first rows of the warp's first lane of each position
         Pair f[H], k[H], s[2 * H];
         const int first = min(p.n, kFirstRows);
@@ -390,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_tile_kernel(const NormProble
                 s[H + j] = fma2(d, d, s[H + j]);
             }
         }
-        put_row_sums<H, LPR_LOG>(s, part[threadIdx.x / 32], p.lpr_log, p.lane, p.sub);
+        put_row_sums<H, -1, kTW>(s, part[threadIdx.x / 32], p.lpr_log, p.lane, p.sub);
         if (p.lane < (1 << p.lpr_log))
 #pragma unroll
             for (int j = 0; j < H; ++j) {
@@ -415,15 +388,14 @@ __global__ void __launch_bounds__(kThreads, 3) norm_tile_kernel(const NormProble
                     m = *cluster.map_shared_rank(&own[turn][col], g);
                 m = join8(m, g < t.split ? (float)max(0, min(t.slice, (int)P.C - g * t.slice)) : 0.0f);
             }
-            const float off = m.s1 * t.inv_c, var = fmaxf(m.s2 * t.inv_c - off * off, 0.0f);
-            const float rstd = 1.0f / sqrtf((m.s2 == m.s2 ? var : m.s2) + P.eps);   // fmaxf drops NaN
             if (g == 0) {
-                stat[col] = make_float2(-(m.k + off), rstd);
+                const float2 q = finish(m, t, P.eps);
+                stat[col] = q;
                 if (rank == 0 && col < min((int64_t)t.tw, left)) {
                     if (P.mean)
-                        P.mean[w.b * P.L + l0 + col] = m.k + off;
+                        P.mean[w.b * P.L + l0 + col] = -q.x;
                     if (P.rstd)
-                        P.rstd[w.b * P.L + l0 + col] = rstd;
+                        P.rstd[w.b * P.L + l0 + col] = q.y;
                 }
             }
         }
@@ -435,9 +407,6 @@ __global__ void __launch_bounds__(kThreads, 3) norm_tile_kernel(const NormProble
             k[j] = pair(u.x, v.x);
             rstd[j] = pair(u.y, v.y);
         }
-        const bool in = p.sub * V < left;
-        T *y = static_cast<T *>(P.y) + base + p.row * P.L + p.sub * V;
-        int8_t *codes = P.codes + base + p.row * P.L + p.sub * V;
         uint8_t *scale = P.scales + (w.b * P.C + c0 + p.row) * nb + l0 / kCkBlock;
         // CK: whole warps walk together, for the block maximum's shuffles
         const int n = CK ? p.warp_n : p.n;
@@ -453,204 +422,118 @@ __global__ void __launch_bounds__(kThreads, 3) norm_tile_kernel(const NormProble
                 v[j] = mul2(add2(v[j], k[j]), rstd[j]);
                 f[j] = fma2(v[j], g, be);
             }
-            const uint4 o = pairs_to_chunk<T>(f);
-            if constexpr (!VEC) {
-                if (row)
-                    mine[r * kThreads] = o;
-            } else {
-                if (row && in)
-                    *reinterpret_cast<uint4 *>(y) = o;
-                y += hop;
-            }
+            if (row)
+                mine[r * kThreads] = pairs_to_chunk<T>(f);
             if constexpr (CK) {
                 float top = 0.0f;
 #pragma unroll
-                for (int j = 0; j < H; ++j) {
+                for (int j = 0; j < H; ++j) {  // without the values past the row's end
                     float2 a = halves(v[j]);
-                    if constexpr (!VEC) {      // values past the row's end
-                        a.x = p.sub * V + 2 * j < left ? a.x : 0.0f;
-                        a.y = p.sub * V + 2 * j + 1 < left ? a.y : 0.0f;
-                        v[j] = pair(a.x, a.y);
-                    }
+                    a.x = p.sub * V + 2 * j < left ? a.x : 0.0f;
+                    a.y = p.sub * V + 2 * j + 1 < left ? a.y : 0.0f;
+                    v[j] = pair(a.x, a.y);
                     top = max_abs(max_abs(top, a.x), a.y);
                 }
-                uint32_t bits = row && in ? ck_abs_bits(top) : 0u;
-                if constexpr (LPR_LOG >= 0) {
-#pragma unroll
-                    for (int o2 = 1; o2 < (1 << LPR_LOG); o2 <<= 1)
-                        bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o2));
-                } else {
-                    for (int o2 = 1; o2 < lanes; o2 <<= 1)
-                        bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o2));
-                }
+                uint32_t bits = row ? ck_abs_bits(top) : 0u;
+                for (int o = 1; o < (1 << p.lpr_log); o <<= 1)   // a tile's row is a block of codes
+                    bits = max(bits, __shfl_xor_sync(0xFFFFFFFFu, bits, o));
                 const uint32_t e = ck_scale(bits, ck_top<float>());
                 uint32_t q[V / 4];
                 code_pairs<H>(v, ck_inverse(e), q);
-                if constexpr (!VEC)
-                    put_code_words<V>(ctile + (threadIdx.x + r * kThreads) * V, q);
-                else if (row && in)
-                    put_code_words<V>(codes, q);
+                put_code_words<V>(ctile + (threadIdx.x + r * kThreads) * V, q);
                 if (row && p.sub == 0)
-                    *scale = (uint8_t)e;
-                codes += hop;
-                scale += scale_hop;
+                    scale[r * p.stride * nb] = (uint8_t)e;
             }
         }
-        if constexpr (!VEC) {
-            __syncwarp();
-            store_rows<T, V>(reinterpret_cast<T *>(tile4), static_cast<T *>(P.y) + base, P.L, left,
-                             nrow, t, p);
-            if constexpr (CK)
-                store_rows<int8_t, V>(ctile, P.codes + base, P.L, left, nrow, t, p);
-            __syncwarp();   // the next tile's values overwrite what the warp has read
-        }
+        __syncwarp();
+        store_rows<T, V>(tile, static_cast<T *>(P.y) + base, P.L, left, nrow, t, p);
+        if constexpr (CK)
+            store_rows<int8_t, V>(ctile, P.codes + base, P.L, left, nrow, t, p);
+        __syncwarp();   // the next tile's values overwrite what the warp has read
     }
     if (t.split > 1)
         cg::this_cluster().sync();   // another block may still read this one's `own`
 }
 
-// Shared memory of the forward's tile kernel for a channel: two tiles, or one and its codes.
-template <class T>
-constexpr int norm_row_bytes(int tw, bool vec, bool ck) {
-    return tw * (vec ? 2 * (int)sizeof(T) : (int)sizeof(T) + (ck ? 1 : 0));
+// Shared memory of the forward's tile kernel for a channel.
+template <class T> constexpr int norm_row_bytes(int tw, bool ck) {
+    return tw * ((int)sizeof(T) + (ck ? 1 : 0));
 }
 
-// The same of the gradient's: grad_y and x (or codes) of two tiles or one, each lane's sums
-// of grad_y v and grad_y of its rows, and gamma with the step of the codes.
-template <class T>
-constexpr int grad_row_bytes(int tw, bool vec, bool ck) {
-    const int V = 16 / (int)sizeof(T);
-    return (vec ? 2 : 1) * tw * ((int)sizeof(T) + (ck ? 1 : (int)sizeof(T))) + tw / V * 8 + 8;
+// The same of the gradient's: grad_y and x (or codes), each lane's sums of grad_y v and
+// grad_y of its rows, and gamma with the step of the codes.
+template <class T> constexpr int grad_row_bytes(int tw, bool ck) {
+    return tw * ((int)sizeof(T) + (ck ? 1 : (int)sizeof(T))) + tw / Vec<T>::V * 8 + 8;
 }
 
-constexpr int kStepRegs = 4;   // step bytes a lane holds of the next tile
-constexpr int kMaxSlice = kStepRegs * kThreads;
-
-// grad_x tile by tile.  A cluster of t.split blocks walks tiles cluster, cluster + n, ...;
-// each lane's sums of grad_y v and grad_y over its rows and the walk stay in shared memory
-// (one addition a row and tile instead of a shuffle tree) and are joined at the end into
-// the cluster's rows of `part_g` [clusters][2][C]: a fixed order, no atomics.
-template <class T, bool VEC, bool CK, int LPR_LOG>
+// A cluster of t.split blocks walks tiles cluster, cluster + n, ...; each lane's sums of
+// grad_y v and grad_y over its rows and the walk stay in shared memory and are joined at
+// the end into the cluster's rows of `part_g` [clusters][2][C]: a fixed order, no atomics.
+template <class T, bool CK>
 __global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormGrad P,
                                                                      const Tiling t,
                                                                      float *part_g) {
-    constexpr int V = Vec<T>::V, H = Vec<T>::H, STAGES = VEC ? 2 : 1;
-    extern __shared__ uint4 tile4[];           // chunks of grad_y, then of x / codes, by stages
+    constexpr int V = Vec<T>::V, H = Vec<T>::H;
+    extern __shared__ uint4 tile4[];           // chunks of grad_y, then of x / codes
     __shared__ __align__(8) float part[kWarps][2 * kTW];
     __shared__ float2 own[2][kTW];
     __shared__ float2 stat[kTW];               // (-A, -S)
     const int rank = t.split > 1 ? blockIdx.x % t.split : 0;
     const unsigned cluster_at = t.split > 1 ? blockIdx.x / t.split : blockIdx.x;
-    Walk w(t, cluster_at), ahead = w;
     const int c0 = rank * t.slice;
     const int nrow = min(t.slice, (int)P.C - c0);
-    const Place<LPR_LOG> p(t, nrow);
-    const int chunks = t.slice << p.lpr_log;   // of a tile
+    const Place<-1> p(t, nrow);
+    const int chunks = t.slice << p.lpr_log;
     T *gtile = reinterpret_cast<T *>(tile4);
-    uint4 *after = tile4 + STAGES * chunks;
+    uint4 *after = tile4 + chunks;
     T *xtile = reinterpret_cast<T *>(after);
     int8_t *ctile = reinterpret_cast<int8_t *>(after);
-    unsigned char *at_byte = reinterpret_cast<unsigned char *>(after) +
-                             (size_t)STAGES * chunks * V * (CK ? 1 : sizeof(T));
-    Pair *acc = reinterpret_cast<Pair *>(at_byte);                    // a chunk
+    Pair *acc = reinterpret_cast<Pair *>(reinterpret_cast<unsigned char *>(after) +
+                                         (size_t)chunks * V * (CK ? 1 : sizeof(T)));   // a chunk
     float2 *scaled = reinterpret_cast<float2 *>(acc + chunks);        // a row: gamma, step
     const int64_t nb = ck_blocks(P.L);
     const T *gamma = P.gamma ? static_cast<const T *>(P.gamma) + c0 : nullptr;
-    // the warp's rows, one a lane: rows first, first + rows_hop, ... are this lane's to fetch
-    // gamma and the steps of
-    const int rows_log = 5 - p.lpr_log;
-    const int first = ((int)(threadIdx.x & ~31u) >> p.lpr_log) + (p.lane >> rows_log) * p.stride +
-                      (p.lane & ((1 << rows_log) - 1));
-    const int rows_hop = p.stride << p.lpr_log;
-    for (int r = 0; r < p.n; ++r)
+    for (int r = 0; r < p.n; ++r) {
         acc[threadIdx.x + r * kThreads] = 0;
-    for (int i = first; i < nrow; i += rows_hop)
-        scaled[i] = make_float2(gamma ? ld_f32(gamma + i) : 1.0f, 1.0f);
-    uint8_t step[kStepRegs] = {};
-    auto load = [&](const Walk &at, int stage) {
-        const int64_t l0 = (int64_t)at.lt << t.tw_log, base = (at.b * P.C + c0) * P.L + l0;
-        load_rows<T, V, VEC>(gtile + stage * chunks * V, static_cast<const T *>(P.gy) + base, P.L,
-                             P.L - l0, nrow, t, p);
-        if constexpr (CK) {
-            load_rows<int8_t, V, VEC>(ctile + stage * chunks * V, P.codes + base, P.L, P.L - l0,
-                                      nrow, t, p);
-            const uint8_t *from = P.scales + (at.b * P.C + c0) * nb + l0 / kCkBlock;
-#pragma unroll
-            for (int r = 0; r < kStepRegs; ++r)
-                if (first + r * rows_hop < nrow)
-                    step[r] = from[(first + r * rows_hop) * nb];
-        } else {
-            load_rows<T, V, VEC>(xtile + stage * chunks * V, static_cast<const T *>(P.x) + base,
-                                 P.L, P.L - l0, nrow, t, p);
-        }
-    };
-    if constexpr (VEC) {
-        load(w, 0);
-        copies_issued();
+        const int i = p.row + r * p.stride;
+        if (p.sub == 0)
+            scaled[i] = make_float2(gamma ? ld_f32(gamma + i) : 1.0f, 1.0f);
     }
+    const uint4 *gmine = tile4 + threadIdx.x, *xmine = after + threadIdx.x;
+    const int8_t *cmine = ctile + threadIdx.x * V;
+    const float2 *smine = scaled + p.row;
     int turn = 0;
-    for (; w.b < P.B; w.step(t), turn ^= 1) {
+    for (Walk w(t, cluster_at); w.b < P.B; w.step(t), turn ^= 1) {
         const int64_t l0 = (int64_t)w.lt << t.tw_log;
         const int64_t left = P.L - l0;
         const int64_t base = (w.b * P.C + c0) * P.L + l0;
-        const bool in = p.sub * V < left;
-        const int stage = VEC ? turn : 0;
-        if constexpr (!VEC)
-            load(w, 0);
-        if constexpr (CK)                      // every lane has read the last tile's steps
-#pragma unroll
-            for (int r = 0; r < kStepRegs; ++r)
-                if (first + r * rows_hop < nrow)
-                    scaled[first + r * rows_hop].y = ck_step(step[r]);
+        load_rows<T, V>(gtile, static_cast<const T *>(P.gy) + base, P.L, left, nrow, t, p);
+        if constexpr (CK) {
+            load_rows<int8_t, V>(ctile, P.codes + base, P.L, left, nrow, t, p);
+            const uint8_t *from = P.scales + (w.b * P.C + c0 + p.row) * nb + l0 / kCkBlock;
+            if (p.sub == 0)
+#pragma unroll 4
+                for (int r = 0; r < p.n; ++r)
+                    scaled[p.row + r * p.stride].y = ck_step(from[r * p.stride * nb]);
+        } else {
+            load_rows<T, V>(xtile, static_cast<const T *>(P.x) + base, P.L, left, nrow, t, p);
+        }
         Pair rstd[H], neg[H];                  // neg: minus the mean
         const float *rs = P.rstd + w.b * P.L + l0 + p.sub * V, *me = nullptr;
         if constexpr (!CK)
             me = P.mean + w.b * P.L + l0 + p.sub * V;
-        if constexpr (VEC) {
 #pragma unroll
-            for (int j = 0; j < H; j += 2) {
-                float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = u;
-                if (in) {
-                    u = __ldg(reinterpret_cast<const float4 *>(rs) + j / 2);
-                    if constexpr (!CK)
-                        v = __ldg(reinterpret_cast<const float4 *>(me) + j / 2);
-                }
-                rstd[j] = pair(u.x, u.y);
-                rstd[j + 1] = pair(u.z, u.w);
-                neg[j] = pair(-v.x, -v.y);
-                neg[j + 1] = pair(-v.z, -v.w);
-            }
-            ahead.step(t);
-            if (ahead.b < P.B)
-                load(ahead, stage ^ 1);
-            copies_issued();
-            earlier_copies_landed();
-        } else {
-#pragma unroll
-            for (int j = 0; j < V; j += 2) {
-                const bool u = p.sub * V + j < left, v = p.sub * V + j + 1 < left;
-                rstd[j / 2] = pair(u ? __ldg(rs + j) : 0.0f, v ? __ldg(rs + j + 1) : 0.0f);
-                neg[j / 2] = 0;
-                if constexpr (!CK)
-                    neg[j / 2] = pair(u ? -__ldg(me + j) : 0.0f, v ? -__ldg(me + j + 1) : 0.0f);
-            }
-            copies_landed();
+        for (int j = 0; j < V; j += 2) {
+            const bool u = p.sub * V + j < left, v = p.sub * V + j + 1 < left;
+            rstd[j / 2] = pair(u ? __ldg(rs + j) : 0.0f, v ? __ldg(rs + j + 1) : 0.0f);
+            neg[j / 2] = 0;
+            if constexpr (!CK)
+                neg[j / 2] = pair(u ? -__ldg(me + j) : 0.0f, v ? -__ldg(me + j + 1) : 0.0f);
         }
+        copies_landed();
         __syncwarp();
-        const uint4 *gmine = tile4 + stage * chunks + threadIdx.x;
-        const int8_t *cmine = ctile + (stage * chunks + threadIdx.x) * V;
-        const uint4 *xmine = reinterpret_cast<const uint4 *>(xtile) + stage * chunks + threadIdx.x;
-        const float2 *smine = scaled + p.row;
-        // the checkpoint's v is h step, with one step a row: gamma gy v = (gy h) (gamma step)
-        Pair s[2 * H];
-#pragma unroll
-        for (int j = 0; j < 2 * H; ++j)
-            s[j] = 0;
-#pragma unroll 2
-        for (int r = 0; r < p.n; ++r) {
-            Pair g[H], h[H], sg = 0, sb = 0;
-            chunk_to_pairs<T>(gmine[r * kThreads], g);
-            const float2 f = smine[r * p.stride];
+        // v of a row's chunk, but for the step of its codes
+        auto values = [&](int r, Pair (&h)[H]) {
             if constexpr (CK) {
                 uint32_t words[V / 4];
                 code_words<V>(cmine + r * kThreads * V, words);
@@ -661,6 +544,18 @@ __global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormG
                 for (int j = 0; j < H; ++j)
                     h[j] = mul2(add2(h[j], neg[j]), rstd[j]);
             }
+        };
+        // the checkpoint's v is h step, with one step a row: gamma gy v = (gy h) (gamma step)
+        Pair s[2 * H];
+#pragma unroll
+        for (int j = 0; j < 2 * H; ++j)
+            s[j] = 0;
+#pragma unroll 2
+        for (int r = 0; r < p.n; ++r) {
+            Pair g[H], h[H], sg = 0, sb = 0;
+            chunk_to_pairs<T>(gmine[r * kThreads], g);
+            const float2 f = smine[r * p.stride];
+            values(r, h);
             const Pair w2 = twice(f.x), ws = twice(CK ? f.x * f.y : f.x);
 #pragma unroll
             for (int j = 0; j < H; ++j) {
@@ -677,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormG
             }
         }
         if (P.gx) {
-            put_row_sums<H, LPR_LOG>(s, part[threadIdx.x / 32], p.lpr_log, p.lane, p.sub);
+            put_row_sums<H, -1, kTW>(s, part[threadIdx.x / 32], p.lpr_log, p.lane, p.sub);
             __syncthreads();
             {   // eight threads a position, one a warp's sums
                 const int col = threadIdx.x / 8, g = threadIdx.x % 8;
@@ -706,42 +601,23 @@ __global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormG
                 rA[j] = mul2(pair(u.x, v.x), rstd[j]);
                 rS[j] = mul2(pair(u.y, v.y), rstd[j]);
             }
-            T *out = static_cast<T *>(P.gx) + base + p.row * P.L + p.sub * V;
-            const int64_t hop = p.stride * P.L;
 #pragma unroll 2
             for (int r = 0; r < p.n; ++r) {
                 Pair g[H], h[H];
                 chunk_to_pairs<T>(gmine[r * kThreads], g);
                 const float2 f = smine[r * p.stride];
-                const Pair w2 = twice(f.x);
-                if constexpr (CK) {
-                    uint32_t words[V / 4];
-                    code_words<V>(cmine + r * kThreads * V, words);
-                    codes_to_pairs<H>(words, h);
-                    const Pair st = twice(f.y);
+                values(r, h);
+                const Pair w2 = twice(f.x), st = twice(f.y);   // st: 1 without a checkpoint
 #pragma unroll
-                    for (int j = 0; j < H; ++j)
+                for (int j = 0; j < H; ++j) {
+                    if constexpr (CK)
                         h[j] = mul2(h[j], st);
-                } else {
-                    chunk_to_pairs<T>(xmine[r * kThreads], h);
-#pragma unroll
-                    for (int j = 0; j < H; ++j)
-                        h[j] = mul2(add2(h[j], neg[j]), rstd[j]);
-                }
-#pragma unroll
-                for (int j = 0; j < H; ++j)
                     g[j] = fma2(h[j], rS[j], fma2(mul2(g[j], w2), rstd[j], rA[j]));
-                const uint4 u = pairs_to_chunk<T>(g);
-                if constexpr (!VEC)
-                    tile4[threadIdx.x + r * kThreads] = u;
-                else if (in)
-                    *reinterpret_cast<uint4 *>(out) = u;
-                out += hop;
+                }
+                tile4[threadIdx.x + r * kThreads] = pairs_to_chunk<T>(g);
             }
-            if constexpr (!VEC) {
-                __syncwarp();
-                store_rows<T, V>(gtile, static_cast<T *>(P.gx) + base, P.L, left, nrow, t, p);
-            }
+            __syncwarp();
+            store_rows<T, V>(gtile, static_cast<T *>(P.gx) + base, P.L, left, nrow, t, p);
         }
         __syncwarp();   // the next tile's values and steps overwrite what the warp has read
     }
@@ -792,13 +668,9 @@ __global__ void __launch_bounds__(kThreads, 4) norm_stream_kernel(const NormProb
     const T *safe = static_cast<const T *>(P.x) + w.b * P.C * P.L;
     const T *x0 = in && p.n > 0 ? static_cast<const T *>(P.x) + base + p.row * P.L + p.sub * V : safe;
     const int64_t hop = p.stride * P.L, x_hop = in ? hop : 0;
-    if (p.lane == 0) {
-        const int first = (int)threadIdx.x >> p.lpr_log, rows = 32 >> p.lpr_log;
-        int n = 0;                             // rows of the warp
-        for (int i = first; i < nrow; i += p.stride)
-            n += min(rows, nrow - i);
-        count[threadIdx.x / 32] = (float)n;
-    }
+    const float rows = warp_rows(p, nrow);
+    if (p.lane == 0)
+        count[threadIdx.x / 32] = rows;
     auto chunk = [](const T *at) { return __ldg(reinterpret_cast<const uint4 *>(at)); };
     // k: the mean of the first rows of the warp's first lane of each position
     Pair f[H], k[H], s[2 * H];
@@ -871,15 +743,14 @@ __global__ void __launch_bounds__(kThreads, 4) norm_stream_kernel(const NormProb
                 m = *cg::this_cluster().map_shared_rank(&own[c], g);
             m = join8(m, g < t.split ? (float)max(0, min(t.slice, (int)P.C - g * t.slice)) : 0.0f);
         }
-        const float off = m.s1 * t.inv_c, var = fmaxf(m.s2 * t.inv_c - off * off, 0.0f);
-        const float rstd = 1.0f / sqrtf((m.s2 == m.s2 ? var : m.s2) + P.eps);   // fmaxf drops NaN
         if (g == 0) {
-            stat[c] = make_float2(-(m.k + off), rstd);
+            const float2 q = finish(m, t, P.eps);
+            stat[c] = q;
             if (rank == 0 && c < left) {
                 if (P.mean)
-                    P.mean[w.b * P.L + l0 + c] = m.k + off;
+                    P.mean[w.b * P.L + l0 + c] = -q.x;
                 if (P.rstd)
-                    P.rstd[w.b * P.L + l0 + c] = rstd;
+                    P.rstd[w.b * P.L + l0 + c] = q.y;
             }
         }
     }
@@ -1521,6 +1392,9 @@ __global__ void __launch_bounds__(kThreads) norm_grad_any_kernel(const NormGrad 
     const int rows = kThreads / TL, row0 = threadIdx.x / TL;
     const bool along_c = P.L == 1;
     const int64_t nb = ck_blocks(along_c ? P.C : P.L);
+    const int64_t total = P.B * P.C * P.L;
+    // every access is checked: free next to the rest, in a kernel for sizes that are rarely run
+    auto inside = [&](int64_t at) { return at >= 0 && at < total; };
     float *pg = part_g ? part_g + (int64_t)blockIdx.x * 2 * P.C : nullptr;
     for (int64_t tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
         const int64_t b = tile / tiles, l = (tile - b * tiles) * TL + col;
@@ -1529,6 +1403,8 @@ __global__ void __launch_bounds__(kThreads) norm_grad_any_kernel(const NormGrad 
         const float mean = !CK && in ? P.mean[b * P.L + l] : 0.0f;
         auto value = [&](int64_t c) {
             const int64_t at = (b * P.C + c) * P.L + l;
+            if (!inside(at))
+                return 0.0f;
             if (CK)
                 return (float)P.codes[at] *
                        ck_step(P.scales[along_c ? b * nb + c / kCkBlock
@@ -1540,7 +1416,7 @@ __global__ void __launch_bounds__(kThreads) norm_grad_any_kernel(const NormGrad 
         for (int64_t c0 = 0; c0 < P.C; c0 += rows) {
             const int64_t c = c0 + row0;
             float g = 0.0f, v = 0.0f;
-            if (in && c < P.C) {
+            if (in && c < P.C && inside((b * P.C + c) * P.L + l)) {
                 g = ld_f32(gy + (b * P.C + c) * P.L + l);
                 v = value(c);
                 const float d = P.gamma ? g * ld_f32(static_cast<const T *>(P.gamma) + c) : g;
@@ -1564,7 +1440,7 @@ __global__ void __launch_bounds__(kThreads) norm_grad_any_kernel(const NormGrad 
             const float A = sum_over_rows(a, TL, part) / (float)P.C;
             const float S = sum_over_rows(q, TL, part) / (float)P.C;
             if (in)
-                for (int64_t c = row0; c < P.C; c += rows) {
+                for (int64_t c = row0; c < P.C && inside((b * P.C + c) * P.L + l); c += rows) {
                     const float g = ld_f32(gy + (b * P.C + c) * P.L + l);
                     const float d = P.gamma ? g * ld_f32(static_cast<const T *>(P.gamma) + c) : g;
                     static_cast<T *>(P.gx)[(b * P.C + c) * P.L + l] =
@@ -1636,7 +1512,7 @@ bool make_tiling(int64_t B, int64_t C, int64_t L, int size, int most, Bytes row_
     t->split = 1;
     while (t->split < kMaxSplit && shared(t->split) > 69 * 1024)
         t->split *= 2;
-    if (shared(t->split) > 200 * 1024 || (most == kTW && slice(t->split) > kMaxSlice))
+    if (shared(t->split) > 200 * 1024)
         return false;
     while (t->split < kMaxSplit && t->total * t->split < sm_count_or(148) &&
            slice(t->split) >= 2 * rows)
@@ -1710,7 +1586,6 @@ cudaError_t norm(const NormProblem &P, cudaStream_t s) {
     }
     Tiling t;
     const bool vec = base && P.L % V == 0;
-    auto row_bytes = [&](int tw) { return norm_row_bytes<T>(tw, vec, P.codes != nullptr); };
     constexpr int WIDE = 128 / (int)sizeof(T);
     if (vec && make_tiling(P.B, P.C, P.L, sizeof(T), WIDE, [](int) { return 0; }, &t)) {
         const bool full = t.tw == WIDE;
@@ -1719,19 +1594,14 @@ cudaError_t norm(const NormProblem &P, cudaStream_t s) {
                                       : norm_stream_kernel<T, false, -1>);
         return launch_cluster(kernel, (unsigned)(t.total * t.split), (unsigned)t.split, 0, s, P, t);
     }
-    if (make_tiling(P.B, P.C, P.L, sizeof(T), kTW, row_bytes, &t)) {
+    auto row_bytes = [&](int tw) { return norm_row_bytes<T>(tw, P.codes != nullptr); };
+    if (!vec && make_tiling(P.B, P.C, P.L, sizeof(T), kTW, row_bytes, &t)) {
         const size_t shared = (size_t)t.slice * row_bytes(t.tw);
-        const unsigned grid = (unsigned)(plan_walk(&t, (int64_t)sm_count_or(148) * blocks_per_sm(shared) / t.split) * t.split);
-        constexpr int FULL = sizeof(T) == 2 ? 2 : 3;   // log2 of the lanes of a full row
-        const bool full = vec && t.tw == kTW;
-        auto kernel =
-            P.codes ? (full ? norm_tile_kernel<T, true, true, FULL>
-                            : vec ? norm_tile_kernel<T, true, true, -1>
-                                  : norm_tile_kernel<T, false, true, -1>)
-                    : (full ? norm_tile_kernel<T, true, false, FULL>
-                            : vec ? norm_tile_kernel<T, true, false, -1>
-                                  : norm_tile_kernel<T, false, false, -1>);
-        return launch_cluster(kernel, grid, (unsigned)t.split, shared, s, P, t);
+        const unsigned grid = (unsigned)(plan_walk(&t, (int64_t)sm_count_or(148) *
+                                                           blocks_per_sm(shared) / t.split) *
+                                         t.split);
+        return launch_cluster(P.codes ? norm_tile_kernel<T, true> : norm_tile_kernel<T, false>, grid,
+                              (unsigned)t.split, shared, s, P, t);
     }
     const int TL = lanes_along(P.L);
     norm_any_kernel<T><<<(unsigned)(P.B * ((P.L + TL - 1) / TL)), kThreads, 0, s>>>(P, TL);
@@ -1740,9 +1610,8 @@ cudaError_t norm(const NormProblem &P, cudaStream_t s) {
 
 // How a backward runs: the kernel family, its blocks, and the rows of partial sums.
 struct GradPlan {
-    int kind;          // 0: any sizes, 1: tiles, 2: a warp a row, 3: a block a row
+    int kind;          // 0: any sizes, 1: tiles, 2: a warp a row, 3: a block a row, 4: streams
     int nv;
-    bool vec;
     Tiling t;
     size_t shared;
     int64_t blocks, rows;
@@ -1769,8 +1638,8 @@ GradPlan grad_plan(const NormGrad &P) {
             return g;
         }
     }
-    g.vec = base && P.L % V == 0;
-    if (g.vec && make_tiling(P.B, P.C, P.L, sizeof(T), 128 / (int)sizeof(T),
+    const bool vec = base && P.L % V == 0;
+    if (vec && make_tiling(P.B, P.C, P.L, sizeof(T), 128 / (int)sizeof(T),
                              [](int) { return (int)(sizeof(float) * 3); }, &g.t)) {
         g.kind = 4;
         g.shared = (size_t)g.t.slice * sizeof(float) * 3;
@@ -1779,8 +1648,8 @@ GradPlan grad_plan(const NormGrad &P) {
         g.blocks = g.rows * g.t.split;
         return g;
     }
-    auto row_bytes = [&](int tw) { return grad_row_bytes<T>(tw, g.vec, P.from_codes); };
-    if (make_tiling(P.B, P.C, P.L, sizeof(T), kTW, row_bytes, &g.t)) {
+    auto row_bytes = [&](int tw) { return grad_row_bytes<T>(tw, P.from_codes); };
+    if (!vec && make_tiling(P.B, P.C, P.L, sizeof(T), kTW, row_bytes, &g.t)) {
         g.kind = 1;
         g.shared = (size_t)g.t.slice * row_bytes(g.t.tw);
         g.rows = plan_walk(&g.t, (int64_t)sms * blocks_per_sm(g.shared) / g.t.split);
@@ -1801,10 +1670,8 @@ cudaError_t run_norm_grad(const NormGrad &P, const GradPlan &g, float *part, cud
                                                              : norm_grad_stream_kernel<T, CK, -1>,
                               grid, (unsigned)g.t.split, g.shared, s, P, g.t, part);
     if (g.kind == 1)
-        return launch_cluster(!g.vec              ? norm_grad_tile_kernel<T, false, CK, -1>
-                              : g.t.tw == kTW ? norm_grad_tile_kernel<T, true, CK, sizeof(T) == 2 ? 2 : 3>
-                                              : norm_grad_tile_kernel<T, true, CK, -1>,
-                              grid, (unsigned)g.t.split, g.shared, s, P, g.t, part);
+        return launch_cluster(norm_grad_tile_kernel<T, CK>, grid, (unsigned)g.t.split, g.shared, s, P,
+                              g.t, part);
     if (g.kind >= 2) {
         auto kernel = g.kind == 2 ? (g.nv == 1   ? norm_grad_row_kernel<T, 32, 1, CK>
                                      : g.nv == 2 ? norm_grad_row_kernel<T, 32, 2, CK>
