@@ -155,7 +155,7 @@ int validate_backward(const dcn1d_tensor *x, const dcn1d_tensor *off, const dcn1
                       int64_t padding_right, int64_t dilation, int64_t groups, int64_t offset_groups,
                       int unconstrained, const dcn1d_tensor *gx, const dcn1d_tensor *goff,
                       const dcn1d_tensor *gmask, const dcn1d_tensor *gw, const dcn1d_tensor *gbias,
-                      Problem *P, BackwardGrads *G) {
+                      Problem *P, BackwardGrads *G, bool *gemm_grid_fits = nullptr) {
     int st = validate(x, off, mask, w, nullptr, stride, padding, padding_right, dilation, groups,
                       offset_groups, unconstrained, gout, P);
     if (st != DCN1D_OK)
@@ -186,7 +186,11 @@ int validate_backward(const dcn1d_tensor *x, const dcn1d_tensor *off, const dcn1
         if (gbias->shape[0] != P->C_out)
             return DCN1D_ERR_SHAPE;
     }
-    if ((int64_t)P->B * P->groups > 65535)   // one GEMM grid slice per (batch, group)
+    // one GEMM grid slice per (batch, group); a caller that may not need the GEMMs asks
+    const bool fits = (int64_t)P->B * P->groups <= 65535;
+    if (gemm_grid_fits)
+        *gemm_grid_fits = fits;
+    else if (!fits)
         return DCN1D_ERR_UNSUPPORTED;
     G->gout = gout->data;
     G->x = gx ? gx->data : nullptr;
@@ -458,6 +462,8 @@ int validate_norm_grad(const dcn1d_tensor *x, const dcn1d_tensor *gamma, const d
             return st;
     if (gx && (st = check_typed(gx, dt, 3, B, C, L)))
         return st;
+    if (gx && gx->data && (gx->data == gy->data || (x && gx->data == x->data)))
+        return DCN1D_ERR_ARG;
     *P = NormGrad{B, C, L, dt, data_of<void>(x), data_of<void>(gamma), gy->data,
                   data_of<float>(mean), data_of<float>(rstd), data_of<int8_t>(codes),
                   data_of<uint8_t>(scales), data_of<void>(gx), data_of<void>(ggamma),
@@ -495,9 +501,10 @@ int validate_checkpoint_backward(
     dcn1d_tensor x = *codes;
     x.dtype = gout->dtype;
     x.data = reinterpret_cast<void *>((uintptr_t)256);   // the workspace's start, set at launch
+    bool gemm_grid_fits;
     if ((st = validate_backward(&x, off, mask, w, gout, stride, padding, padding_right, dilation,
                                 groups, offset_groups, unconstrained, gx, goff, gmask, gw, gbias,
-                                &R->P, &R->G)))
+                                &R->P, &R->G, &gemm_grid_fits)))
         return st;
     for (const dcn1d_tensor *t : {gamma, beta})
         if (t && (st = check_typed(t, x.dtype, 1, C)))
@@ -505,6 +512,8 @@ int validate_checkpoint_backward(
     R->ck = CkProblem{B, C, L, x.dtype, nullptr, data_of<void>(gamma), data_of<void>(beta),
                       codes->data, scales->data, nullptr};
     R->depthwise = depthwise_grad_supported(R->P);
+    if (!R->depthwise && !gemm_grid_fits)
+        return DCN1D_ERR_UNSUPPORTED;
     R->x_bytes = R->depthwise ? 0 : round256((size_t)(B * C * L) * (x.dtype == DCN1D_F32 ? 4 : 2));
     R->total = R->depthwise ? depthwise_grad_workspace(R->P, R->G)
                             : R->x_bytes + backward_workspace(R->P, R->G);
@@ -1009,6 +1018,8 @@ int dcn1d_layer_norm_forward(const dcn1d_tensor *x, const dcn1d_tensor *gamma,
         return st;
     if (B == 0 || L == 0)
         return DCN1D_OK;
+    if (y->data == x->data)   // x is read a second time
+        return DCN1D_ERR_ARG;
     const NormProblem P{B, C, L, dt, eps, x->data, data_of<void>(gamma), data_of<void>(beta),
                         y->data, data_of<float>(mean), data_of<float>(rstd),
                         data_of<int8_t>(codes), data_of<uint8_t>(scales)};

@@ -44,6 +44,7 @@ struct Args {
     int wpr;                             // warps of a row
     int x_words, sum_words;              // 4-byte words of a row's x and of each sum's array
     int a_bits, b_bits;                  // A and B above (16-bit types: A = 22)
+    bool fixed;                          // they leave a fine enough unit
     bool wide;                           // offsets' gradients leave in 16-byte chunks
     bool even;                           // 16-bit types: two positions' values are whole words
     int64_t rows, nb;
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
         // M < 2^e; the product, associated as the contributions are, may round down twice
         const float tg = bits_to_f32<T>(bg), tm = MASK ? bits_to_f32<T>(bm) : 1.0f;
         const float M = tw * tg * tm;
-        fixed = M < INFINITY && tg < INFINITY && tm < INFINITY && tw < INFINITY;   // false for NaN
+        fixed = a.fixed && M < INFINITY && tg < INFINITY && tm < INFINITY && tw < INFINITY;   // not for NaN
         const int e = (int)((__float_as_uint(M) + 2u) >> 23) - 126;
         s = max(-126, min(126, a.a_bits - e));
         to_hi = two_to(s);
@@ -516,6 +517,7 @@ cudaError_t run(const CheckpointConv &q, void *ws, cudaStream_t s, int *launches
         ++n;
     a.a_bits = sizeof(T) == 2 ? 22 : 30 - n < 21 ? 30 - n : 21;
     a.b_bits = 32 - n < 22 ? 32 - n : 22;
+    a.fixed = sizeof(T) == 2 || n <= 18;
     const int es = P.dtype == DCN1D_F32 ? 4 : 2;
     a.wide = (int64_t)P.L_out * K % (16 / es) == 0 &&
              ((reinterpret_cast<uintptr_t>(G.off) | reinterpret_cast<uintptr_t>(G.mask)) & 15) == 0;

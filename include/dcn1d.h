@@ -427,8 +427,8 @@ const char *dcn1d_packed_forward_kernel_name(
  * L == 1 normalises rows of C contiguous values (single tokens).  Arithmetic and
  * statistics are fp32 (the variance is taken about the mean, in a second pass over values
  * held on chip or read again); y is rounded once.  A position that holds a NaN or an
- * infinity gives NaN at that position only; in the checkpoint it marks its blocks.  One
- * launch, no scratch memory.  Sizes: B * L < 2^31 and C < 2^31; the number of elements
+ * infinity gives NaN at that position only; in the checkpoint it marks its blocks.  x is
+ * read twice: y at x's address is DCN1D_ERR_ARG.  One launch, no scratch memory.  Sizes: B * L < 2^31 and C < 2^31; the number of elements
  * may pass 2^31.
  */
 int dcn1d_layer_norm_forward(const dcn1d_tensor *x, const dcn1d_tensor *gamma,
@@ -445,8 +445,9 @@ int dcn1d_layer_norm_forward(const dcn1d_tensor *x, const dcn1d_tensor *gamma,
  * v comes from x and mean, or from the checkpoint that the forward wrote (x and mean are
  * then NULL): pass x and mean, or codes and scales, not both (DCN1D_ERR_ARG).  rstd and
  * grad_y are required; gamma is the forward's (NULL: 1).  grad_x [B, C, L], grad_gamma and
- * grad_beta [C] are in grad_y's dtype, each NULL when not wanted, and overwritten.  Sums
- * are fp32 in a fixed order: equal calls on one device give equal bits.
+ * grad_beta [C] are in grad_y's dtype, each NULL when not wanted, and overwritten (grad_x
+ * at grad_y's or x's address: DCN1D_ERR_ARG).  Sums are fp32 in a fixed order: equal calls
+ * on one device give equal bits.
  *
  * Scratch: `workspace` (256-byte aligned) of dcn1d_layer_norm_backward_workspace_size()
  * bytes, used only by the work enqueued on `stream`; 0 when neither grad_gamma nor
@@ -506,6 +507,16 @@ int dcn1d_checkpoint_unpack(const dcn1d_tensor *codes, const dcn1d_tensor *scale
  * dtype.  grad_x is the gradient with respect to that x.  All other arguments, errors and
  * remarks as for dcn1d_backward_lr; the workspace (256-byte aligned) has the size that
  * dcn1d_backward_checkpoint_workspace_size gives.
+ *
+ * The depthwise layer with offsets of each channel's own (groups == offset_groups == C_in ==
+ * C_out, K <= 9, L_in up to about 18000 in F32 and 37000 in 16-bit types) runs as one kernel
+ * that reads the checkpoint itself, and a small one that joins the batch for grad_weight and
+ * grad_bias; every sum then has an order-independent value or a fixed order.  Its grad_x is
+ * added in fixed point: with M the largest |mask * weight * grad_out| of a row (b, c), in
+ * multiples of M 2^-22 (16-bit types) or M 2^-26 and finer (F32); rows of more than 2^18 taps
+ * in F32, rows where hundreds of contributions near M meet at one position in 16-bit types,
+ * and rows with a NaN or an infinity add in fp32 (low bits may then differ between calls).
+ * Other layers unpack the checkpoint into the workspace and run dcn1d_backward_lr's kernels.
  */
 int64_t dcn1d_backward_checkpoint_workspace_size(
     const dcn1d_tensor *codes, const dcn1d_tensor *scales, const dcn1d_tensor *gamma,

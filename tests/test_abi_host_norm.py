@@ -26,7 +26,7 @@ def run(name, a, order):
 
 def norm_args(**over):
     a = dict(x=T((B, C, L), BF16), gamma=T((C,), BF16), beta=T((C,), BF16), eps=1e-5,
-             y=T((B, C, L), BF16), mean=T((B, L)), rstd=T((B, L)), codes=T((B, C, L), I8),
+             y=T((B, C, L), BF16, 2 * FAKE), mean=T((B, L)), rstd=T((B, L)), codes=T((B, C, L), I8),
              scales=T((B, C, 2), U8), stream=None)
     a.update(over)
     return a
@@ -58,6 +58,7 @@ BAD_NORM = [
     ("negative eps", dict(eps=-1e-5), 4),
     ("NaN eps", dict(eps=math.nan), 4),
     ("infinite eps", dict(eps=math.inf), 4),
+    ("y in x's place", dict(x=T((B, C, L), BF16, FAKE + 64), y=T((B, C, L), BF16, FAKE + 64)), 4),
     ("too many positions", dict(x=T((1 << 16, 1, 1 << 16), BF16)), 5),
     ("too many channels", dict(x=T((1, 1 << 31, 1), BF16)), 5),
 ]
@@ -80,8 +81,8 @@ def test_single_token_checkpoints_have_blocks_along_the_channels():
 
 
 def grad_args(**over):
-    a = dict(x=T((B, C, L), BF16), gamma=T((C,), BF16), mean=T((B, L)), rstd=T((B, L)),
-             codes=None, scales=None, gy=T((B, C, L), BF16), gx=T((B, C, L), BF16),
+    a = dict(x=T((B, C, L), BF16, 2 * FAKE), gamma=T((C,), BF16), mean=T((B, L)), rstd=T((B, L)),
+             codes=None, scales=None, gy=T((B, C, L), BF16, 3 * FAKE), gx=T((B, C, L), BF16),
              ggamma=T((C,), BF16), gbeta=T((C,), BF16), ws=None, bytes=0, stream=None)
     a.update(over)
     return a
@@ -98,6 +99,8 @@ BAD_GRAD = [
     ("codes alone", dict(KEPT, scales=None), 1),
     ("both x and a checkpoint", dict(codes=T((B, C, L), I8), scales=T((B, C, 2), U8)), 4),
     ("a checkpoint and a mean", dict(KEPT, mean=T((B, L))), 4),
+    ("grad_x in grad_y's place", dict(gy=T((B, C, L), BF16, FAKE)), 4),
+    ("grad_x in x's place", dict(x=T((B, C, L), BF16, FAKE)), 4),
     ("x of another type", dict(x=T((B, C, L), F16)), 2),
     ("grad_x of another type", dict(gx=T((B, C, L), F32)), 2),
     ("rstd of 16 bits", dict(rstd=T((B, L), BF16)), 2),
@@ -224,3 +227,14 @@ def test_binding_refuses_host_tensors_and_unknown_gradients():
         dcn.dcn1d_layer_norm_backward(x, None, s, s, x, wanted=("x", "weight"))
     with pytest.raises(ValueError, match="unknown gradients"):
         dcn.dcn1d_backward_checkpoint((x, x), x, None, x, x, wanted=("gamma",))
+
+
+def test_batches_past_the_gemm_grid_are_the_fused_depthwise_kernels_only():
+    b, c, l = 70, 1000, 8
+    a = dict(codes=T((b, c, l), I8), scales=T((b, c, 1), U8), gamma=None, beta=None,
+             off=T((b, c, l, 3), BF16), w=T((c, 1, 3), BF16), gout=T((b, c, l), BF16), groups=c,
+             og=c, gx=T((b, c, l), BF16), goff=T((b, c, l, 3), BF16), gw=T((c, 1, 3), BF16),
+             gb=T((c,), BF16))
+    assert run("dcn1d_backward_checkpoint_workspace_size", conv_args(**a), CONV) > 0
+    shared = dict(a, og=500, off=T((b, 500, l, 3), BF16), goff=T((b, 500, l, 3), BF16))
+    assert run("dcn1d_backward_checkpoint_workspace_size", conv_args(**shared), CONV) == -5

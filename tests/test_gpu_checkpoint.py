@@ -115,6 +115,10 @@ CONV = {
     "depthwise_nine_taps": ("bf16", 1, 12, 12, 9, 400, 1, 8, 2, 12, 12, False, False, 2.0),
     "depthwise_shared_offsets": ("bf16", 2, 16, 16, 3, 200, 1, 1, 1, 16, 4, True, False, 2.0),
     "depthwise_lout_1": ("f32", 3, 6, 6, 8, 8, 1, 0, 1, 6, 6, False, False, 2.0),
+    "depthwise_many_rows": ("bf16", 70, 1000, 1000, 3, 8, 1, 1, 1, 1000, 1000, False, False, 1.0),
+    "depthwise_wide_padding": ("f32", 1, 2, 2, 3, 50, 1, 60000, 1, 2, 2, True, True, 2.0),
+    "depthwise_long_rows_f32": ("f32", 1, 2, 2, 3, 20000, 1, 1, 1, 2, 2, False, True, 2.0),
+    "depthwise_long_rows": ("f16", 1, 3, 3, 2, 32001, 1, 0, 1, 3, 3, True, False, 1.0),
     "depthwise_far": ("f32", 2, 5, 5, 3, 300, 1, 1, 1, 5, 5, True, True, 400.0),
 }
 NAMES = {"x": "grad_x", "offsets": "grad_offsets", "mask": "grad_mask", "weight": "grad_weight",
