@@ -25,6 +25,13 @@
 //    neither, wherever they meet; the unit is M 2^-30 at 2^16 taps.
 // A row whose M is not finite adds in fp32, so that NaN and infinities reach the sites they
 // belong to.
+//
+// Measured (B200): [8, 512, 16000] bf16, 3 taps, 450 us for 1.11 GB = 2.5 TB/s, 0.38 of the
+// copy bandwidth.  Bound by issue (84 % of the slots, 65 instructions a tap) and by the
+// shared-memory pipe (79 %: the two additions of a tap collide about 4 ways, as offsets
+// scatter the lanes).  Float atomics took 1194 us, two integers a sum 919, one position a
+// lane 542.  512 threads and at most 64 registers for K <= 4: two blocks an SM, so that one
+// unpacks or writes out while the other walks; more taps need the registers.
 #include "checkpoint.cuh"
 #include "pairs.cuh"
 #include "sampler.cuh"
