@@ -1464,30 +1464,37 @@ __global__ void __launch_bounds__(kThreads) norm_grad_any_kernel(const NormGrad 
     }
 }
 
-// grad_gamma[c] and grad_beta[c]: the blocks' partial sums, 32 interleaved chains (few
-// columns, so the chains are what keeps loads in flight) joined in order.
+// grad_gamma[c] and grad_beta[c]: the blocks' partial sums.  A block takes 8 columns (a
+// sector of each row) and 128 interleaved chains of rows, joined in a fixed order: few
+// columns and short chains, so that a few hundred rows are a handful of loads deep.
 template <class T>
 __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float *part, int64_t n,
-                                                               int64_t C, T *ggamma, T *gbeta) {
-    __shared__ float sums[32][33];
+                                                                int64_t C, T *ggamma, T *gbeta) {
+    __shared__ float sums[32][8];
     // launched while the gradient's kernel still runs: wait for its partial sums
     cudaGridDependencySynchronize();
-    const int lane = threadIdx.x & 31, group = threadIdx.x / 32;
-    const int64_t i = (int64_t)blockIdx.x * 32 + lane;
+    const int col = threadIdx.x & 7, chain = threadIdx.x / 8, warp = threadIdx.x / 32;
+    const int64_t i = (int64_t)blockIdx.x * 8 + col;
     float s = 0.0f;
     if (i < 2 * C)
 #pragma unroll 4
-        for (int64_t j = group; j < n; j += 32)
+        for (int64_t j = chain; j < n; j += 128)
             s += part[j * 2 * C + i];
-    sums[group][lane] = s;
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+    if ((threadIdx.x & 31) < 8)
+        sums[warp][col] = s;
     __syncthreads();
-    if (group > 0 || i >= 2 * C)
+    if (warp > 0)
         return;
+    s = 0.0f;
 #pragma unroll
-    for (int g = 1; g < 32; ++g)
-        s += sums[g][lane];
+    for (int k = 0; k < 8; ++k)
+        s += sums[chain * 8 + k][col];         // chain is 0 to 3 here
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
+    s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
     T *out = i < C ? ggamma : gbeta;
-    if (out)
+    if (chain == 0 && i < 2 * C && out)
         out[i < C ? i : i - C] = from_f32<T>(s);
 }
 
@@ -1715,7 +1722,7 @@ cudaError_t norm_grad(const NormGrad &P, void *ws, cudaStream_t s, int *launches
     }
     if (weights) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)((2 * P.C + 31) / 32));
+        cfg.gridDim = dim3((unsigned)((2 * P.C + 7) / 8));
         cfg.blockDim = dim3(1024);
         cfg.stream = s;
         cudaLaunchAttribute attr;
