@@ -44,6 +44,7 @@ struct Tiling {
     int lpr_log;       // log2 of the lanes of a row: tw / V
     int split;         // blocks that share the channels of a tile (a cluster)
     int slice;         // channels of a block, a multiple of the rows of its threads
+    bool words, code_words;   // rows of T, and of codes, are whole 4-byte words
     int walk_b, walk_l;   // a walk's step over (b, tile of b): the number of clusters
     float inv_c;       // 1 / C
     int64_t tiles;     // tiles of one b
@@ -302,7 +303,43 @@ __device__ __forceinline__ float2 finish(const Moments &m, const Tiling &t, floa
 // A tile of 32 positions (fewer when L is shorter) x the block's channels in shared memory,
 // read and written with the lanes along the values, worked on in 16-byte chunks.  Bound by
 // latency at the sizes tested: [3, 381, 1001] fp16 15 us forward and 16 us backward on the
-// device (96 tiles, two blocks each).
+// device (96 tiles, two blocks each).  At [8, 512, ~16000] bf16, where aligned rows take 63 us
+// forward and 96 backward: rows of an even length, as 4-byte words, 120 and 211; odd rows,
+// value by value, 159 and 279.
+
+// The same in 4-byte words of `E` where rows hold whole words (t.words for T,
+// t.code_words for codes): asynchronous copies, and fewer of them.
+template <class E, int V>
+__device__ __forceinline__ void load_tile(E *tile, const E *src, int64_t L, int64_t left, int nrow,
+                                          const Tiling &t, const Place<-1> &p, bool words) {
+    constexpr int N = 4 / (int)sizeof(E);
+    if (N > 1 && words) {
+        Tiling u = t;
+        u.tw = t.tw / N;
+        u.tw_log = t.tw_log - (N == 4 ? 2 : 1);
+        load_rows<uint32_t, V / N>(reinterpret_cast<uint32_t *>(tile),
+                                   reinterpret_cast<const uint32_t *>(src), L / N, (left + N - 1) / N,
+                                   nrow, u, p);
+    } else {
+        load_rows<E, V>(tile, src, L, left, nrow, t, p);
+    }
+}
+
+template <class E, int V>
+__device__ __forceinline__ void store_tile(const E *tile, E *dst, int64_t L, int64_t left, int nrow,
+                                           const Tiling &t, const Place<-1> &p, bool words) {
+    constexpr int N = 4 / (int)sizeof(E);
+    if (N > 1 && words) {
+        Tiling u = t;
+        u.tw = t.tw / N;
+        u.tw_log = t.tw_log - (N == 4 ? 2 : 1);
+        store_rows<uint32_t, V / N>(reinterpret_cast<const uint32_t *>(tile),
+                                    reinterpret_cast<uint32_t *>(dst), L / N, (left + N - 1) / N, nrow,
+                                    u, p);
+    } else {
+        store_rows<E, V>(tile, dst, L, left, nrow, t, p);
+    }
+}
 
 template <class T, bool CK>
 __global__ void __launch_bounds__(kThreads, 3) norm_tile_kernel(const NormProblem P,
@@ -332,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_tile_kernel(const NormProble
         const int64_t l0 = (int64_t)w.lt << t.tw_log;
         const int64_t left = P.L - l0;         // positions of this tile (tw or more: all)
         const int64_t base = (w.b * P.C + c0) * P.L + l0;
-        load_rows<T, V>(tile, static_cast<const T *>(P.x) + base, P.L, left, nrow, t, p);
+        load_tile<T, V>(tile, static_cast<const T *>(P.x) + base, P.L, left, nrow, t, p, t.words);
         copies_landed();
         __syncwarp();
         // k: the mean of the first rows of the warp's first lane of each position
@@ -448,9 +485,9 @@ __global__ void __launch_bounds__(kThreads, 3) norm_tile_kernel(const NormProble
             }
         }
         __syncwarp();
-        store_rows<T, V>(tile, static_cast<T *>(P.y) + base, P.L, left, nrow, t, p);
+        store_tile<T, V>(tile, static_cast<T *>(P.y) + base, P.L, left, nrow, t, p, t.words);
         if constexpr (CK)
-            store_rows<int8_t, V>(ctile, P.codes + base, P.L, left, nrow, t, p);
+            store_tile<int8_t, V>(ctile, P.codes + base, P.L, left, nrow, t, p, t.code_words);
         __syncwarp();   // the next tile's values overwrite what the warp has read
     }
     if (t.split > 1)
@@ -509,16 +546,16 @@ __global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormG
         const int64_t l0 = (int64_t)w.lt << t.tw_log;
         const int64_t left = P.L - l0;
         const int64_t base = (w.b * P.C + c0) * P.L + l0;
-        load_rows<T, V>(gtile, static_cast<const T *>(P.gy) + base, P.L, left, nrow, t, p);
+        load_tile<T, V>(gtile, static_cast<const T *>(P.gy) + base, P.L, left, nrow, t, p, t.words);
         if constexpr (CK) {
-            load_rows<int8_t, V>(ctile, P.codes + base, P.L, left, nrow, t, p);
+            load_tile<int8_t, V>(ctile, P.codes + base, P.L, left, nrow, t, p, t.code_words);
             const uint8_t *from = P.scales + (w.b * P.C + c0 + p.row) * nb + l0 / kCkBlock;
             if (p.sub == 0)
 #pragma unroll 4
                 for (int r = 0; r < p.n; ++r)
                     scaled[p.row + r * p.stride].y = ck_step(from[r * p.stride * nb]);
         } else {
-            load_rows<T, V>(xtile, static_cast<const T *>(P.x) + base, P.L, left, nrow, t, p);
+            load_tile<T, V>(xtile, static_cast<const T *>(P.x) + base, P.L, left, nrow, t, p, t.words);
         }
         Pair rstd[H], neg[H];                  // neg: minus the mean
         const float *rs = P.rstd + w.b * P.L + l0 + p.sub * V, *me = nullptr;
@@ -619,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormG
                 tile4[threadIdx.x + r * kThreads] = pairs_to_chunk<T>(g);
             }
             __syncwarp();
-            store_rows<T, V>(gtile, static_cast<T *>(P.gx) + base, P.L, left, nrow, t, p);
+            store_tile<T, V>(gtile, static_cast<T *>(P.gx) + base, P.L, left, nrow, t, p, t.words);
         }
         __syncwarp();   // the next tile's values and steps overwrite what the warp has read
     }
@@ -1091,7 +1128,9 @@ __global__ void __launch_bounds__(kThreads, 2) norm_grad_stream_kernel(const Nor
 //
 // TPR threads (a warp, or the block) take a row and hold it in registers, NV 16-byte chunks
 // a thread: every value is read once.  One token of 512 channels: 4.3 us on the device, the
-// latency of a launch, one load and two reductions.
+// latency of a launch, one load and two reductions.  16384 rows of 1000 values in bf16: 16 us
+// forward (host included), 28 backward (65 without the next row under way); of 4096, 64 and
+// 100 us, 0.64 of the copy bandwidth.
 
 // Sum over the TPR threads of a row, in every one of them.
 template <int TPR>
@@ -1198,59 +1237,74 @@ __global__ void __launch_bounds__(kThreads) norm_row_kernel(const NormProblem P)
     }
 }
 
-// A thread keeps the weight gradients of its own channels over the block's rows; the warps
-// of a block add theirs in turn.
+// A thread keeps the weight gradients of its own channels over the block's rows; the row
+// after the one in work is on its way.  The rows' groups of a block put theirs side by side
+// in shared memory at the end and are added in order.
 template <class T, int TPR, int NV, bool CK>
-__global__ void __launch_bounds__(kThreads) norm_grad_row_kernel(const NormGrad P, float *part_g) {
+__global__ void __launch_bounds__(kThreads, NV == 4 ? 1 : 2) norm_grad_row_kernel(const NormGrad P,
+                                                                                  float *part_g) {
     constexpr int V = Vec<T>::V, RPB = kThreads / TPR;
-    extern __shared__ float sums[];   // [2][C] (TPR < kThreads)
+    extern __shared__ float sums[];   // [RPB][2][C] (TPR < kThreads)
     __shared__ float part[kWarps];
     const int tid = threadIdx.x % TPR;
     const int C = (int)P.C;
-    const int64_t nb = ck_blocks(C);
+    const int64_t nb = ck_blocks(C), hop = (int64_t)gridDim.x * RPB;
     float ag[NV][V], ab[NV][V];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < V; ++j)
             ag[k][j] = ab[k][j] = 0.0f;
-    for (int64_t b = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; b < P.B;
-         b += (int64_t)gridDim.x * RPB) {
+    struct Row {
+        uint4 g[NV], x[NV];           // CK: x.x, x.y the codes, x.w the step byte
+        float rstd, mean;
+    };
+    auto fetch = [&](int64_t b) {
+        Row u;
         const uint4 *gy = reinterpret_cast<const uint4 *>(static_cast<const T *>(P.gy) + b * C);
-        uint4 u[NV], w[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int i = k * TPR + tid;
-            const bool in = i * V < C;
-            u[k] = w[k] = make_uint4(0, 0, 0, 0);
-            if (in)
-                u[k] = __ldg(gy + i);
-            if constexpr (CK) {
-                if (in) {
-                    *reinterpret_cast<typename CodeWord<V>::type *>(&w[k]) =
-                        reinterpret_cast<const typename CodeWord<V>::type *>(P.codes + b * C)[i];
-                    w[k].w = P.scales[b * nb + i * V / kCkBlock];
+            u.g[k] = u.x[k] = make_uint4(0, 0, 0, 0);
+            if (i * V < C) {
+                u.g[k] = __ldg(gy + i);
+                if constexpr (CK) {
+                    uint32_t q[V / 4];
+                    code_words<V>(P.codes + b * C + i * V, q);
+                    u.x[k].x = q[0];
+                    u.x[k].y = q[V / 4 - 1];
+                    u.x[k].w = __ldg(P.scales + b * nb + i * V / kCkBlock);
+                } else {
+                    u.x[k] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(P.x) + b * C) + i);
                 }
-            } else if (in) {
-                w[k] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(P.x) + b * C) + i);
             }
         }
-        const float rstd = P.rstd[b], mean = CK ? 0.0f : P.mean[b];
+        u.rstd = __ldg(P.rstd + b);
+        u.mean = CK ? 0.0f : __ldg(P.mean + b);
+        return u;
+    };
+    int64_t b = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    Row next;
+    if (b < P.B)
+        next = fetch(b);
+    for (; b < P.B; b += hop) {
+        const Row row = next;
+        if (b + hop < P.B)
+            next = fetch(b + hop);
         auto load = [&](int k, float (&g)[V], float (&v)[V], float (&d)[V]) {
             const int i = k * TPR + tid;
             const bool in = i * V < C;
-            chunk_to_f32<T>(u[k], g);
+            chunk_to_f32<T>(row.g[k], g);
             if constexpr (CK) {
-                const int8_t *q = reinterpret_cast<const int8_t *>(&w[k]);
-                const float step = ck_step(w[k].w);
+                const float step = ck_step(row.x[k].w);
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    v[j] = (float)q[j] * step;
+                    v[j] = (ck_biased((j < 4 ? row.x[k].x : row.x[k].y) ^ 0x80808080u, j % 4) - kCkBias) * step;
             } else {
-                chunk_to_f32<T>(w[k], v);
+                chunk_to_f32<T>(row.x[k], v);
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    v[j] = in ? (v[j] - mean) * rstd : 0.0f;
+                    v[j] = in ? (v[j] - row.mean) * row.rstd : 0.0f;
             }
 #pragma unroll
             for (int j = 0; j < V; ++j)
@@ -1284,7 +1338,7 @@ __global__ void __launch_bounds__(kThreads) norm_grad_row_kernel(const NormGrad 
                 load(k, g, v, d);
 #pragma unroll
                 for (int j = 0; j < V; ++j)
-                    d[j] = rstd * (d[j] - A - v[j] * S);
+                    d[j] = row.rstd * (d[j] - A - v[j] * S);
                 if ((k * TPR + tid) * V < C)
                     gx[k * TPR + tid] = f32_to_chunk<T>(d);
             }
@@ -1293,25 +1347,27 @@ __global__ void __launch_bounds__(kThreads) norm_grad_row_kernel(const NormGrad 
     if (!part_g)
         return;
     float *out = part_g + (int64_t)blockIdx.x * 2 * C;
-    float *to = TPR == kThreads ? out : sums;
-    for (int r = 0; r < RPB; ++r) {
-        if ((int)threadIdx.x / TPR == r)
+    float *to = TPR == kThreads ? out : sums + (threadIdx.x / TPR) * 2 * C;
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int i = k * TPR + tid;
-                if (i * V < C)
+    for (int k = 0; k < NV; ++k) {
+        const int i = k * TPR + tid;
+        if (i * V < C)
 #pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const int c = i * V + j;
-                        to[c] = r == 0 ? ag[k][j] : to[c] + ag[k][j];
-                        to[C + c] = r == 0 ? ab[k][j] : to[C + c] + ab[k][j];
-                    }
+            for (int j = 0; j < V; ++j) {
+                to[i * V + j] = ag[k][j];
+                to[C + i * V + j] = ab[k][j];
             }
-        __syncthreads();
     }
-    if (TPR < kThreads)
-        for (int c = threadIdx.x; c < 2 * C; c += kThreads)
-            out[c] = sums[c];
+    if (TPR < kThreads) {
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * C; c += kThreads) {
+            float v = 0.0f;
+#pragma unroll
+            for (int r = 0; r < RPB; ++r)
+                v += sums[r * 2 * C + c];
+            out[c] = v;
+        }
+    }
 }
 
 // ---------------------------------------------------------------- any sizes
@@ -1617,6 +1673,8 @@ cudaError_t norm(const NormProblem &P, cudaStream_t s) {
     }
     auto row_bytes = [&](int tw) { return norm_row_bytes<T>(tw, P.codes != nullptr); };
     if (!vec && make_tiling(P.B, P.C, P.L, sizeof(T), kTW, row_bytes, &t)) {
+        t.words = P.L * sizeof(T) % 4 == 0 && aligned(P.x, 4) && aligned(P.y, 4);
+        t.code_words = P.L % 4 == 0 && aligned(P.codes, 4);
         const size_t shared = (size_t)t.slice * row_bytes(t.tw);
         const unsigned grid = (unsigned)(plan_walk(&t, (int64_t)sm_count_or(148) *
                                                            blocks_per_sm(shared) / t.split) *
@@ -1653,9 +1711,10 @@ GradPlan grad_plan(const NormGrad &P) {
         if (warp || block) {
             g.kind = warp ? 2 : 3;
             g.nv = warp ? warp : block;
-            g.shared = warp ? 2 * P.C * sizeof(float) : 0;
+            g.shared = warp ? kWarps * 2 * P.C * sizeof(float) : 0;
             const int64_t need = warp ? (P.B + kWarps - 1) / kWarps : P.B;
-            g.blocks = g.rows = need < 2 * sms ? need : 2 * sms;
+            const int64_t room = g.nv == 4 ? sms : 2 * sms;   // blocks that are there at once
+            g.blocks = g.rows = need < room ? need : room;
             return g;
         }
     }
@@ -1672,6 +1731,8 @@ GradPlan grad_plan(const NormGrad &P) {
     auto row_bytes = [&](int tw) { return grad_row_bytes<T>(tw, P.from_codes); };
     if (!vec && make_tiling(P.B, P.C, P.L, sizeof(T), kTW, row_bytes, &g.t)) {
         g.kind = 1;
+        g.t.words = P.L * sizeof(T) % 4 == 0 && aligned(P.gy, 4) && aligned(P.gx, 4) && aligned(P.x, 4);
+        g.t.code_words = P.L % 4 == 0 && aligned(P.codes, 4);
         g.shared = (size_t)g.t.slice * row_bytes(g.t.tw);
         g.rows = plan_walk(&g.t, (int64_t)sms * blocks_per_sm(g.shared) / g.t.split);
         g.blocks = g.rows * g.t.split;

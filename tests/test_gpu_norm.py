@@ -15,7 +15,9 @@ TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
 SHAPES = [(1, 1, 1), (1, 512, 1), (3, 33, 1), (5, 1024, 1), (70, 96, 1), (2, 4100, 1),
           (1, 1, 5), (2, 7, 2), (3, 64, 8), (2, 48, 31), (2, 256, 32), (2, 37, 33),
           (1, 512, 64), (2, 130, 65), (3, 512, 83), (2, 260, 128), (1, 381, 1001),
-          (1, 1030, 40), (1, 2056, 72), (1, 9001, 8), (1, 16, 4096), (4, 256, 200), (1, 26001, 33), (1, 20000, 1)]
+          (1, 1030, 40), (1, 2056, 72), (1, 9001, 8), (1, 16, 4096), (4, 256, 200),
+          (1, 26001, 33), (1, 20000, 1),
+          (2, 70, 50), (3, 200, 36), (1, 40, 14), (3000, 1000, 1), (700, 64, 1), (900, 3000, 1)]
 # the memory that 16-byte accesses need is not there: rows start one element further on
 SHIFTED = [(2, 96, 1), (2, 40, 64), (1, 256, 72)]
 
