@@ -349,3 +349,55 @@ def test_gradients_of_very_different_size_in_one_row(dt):
     for at in range(0, L, 128):
         part = slice(at + 2, at + 126)
         assert ((got - ref)[:, :, part].abs() <= room[:, :, part]).all(), at
+
+
+@pytest.mark.parametrize("key", ["depthwise_bf16_mask_stride", "dense_bf16_mask"])
+def test_calls_from_two_threads_on_their_own_streams(key):
+    """Two host threads, a stream each, many calls at once: scratch is a call's own, so every
+    result is the one of a quiet device (apart by one rounding where dense fp32 atomics came in
+    another order)."""
+    import threading
+    w, t, gout, gamma, beta = conv_case(key)
+    kept = dcn.dcn1d_checkpoint_pack(t["x"])
+
+    def step(stream=None):
+        k = dcn.dcn1d_checkpoint_pack(t["x"], stream=stream)
+        return k, dcn.dcn1d_backward_checkpoint(k, t["offsets"], t["mask"], t["weight"], gout,
+                                                *conv_args(w), gamma=gamma, beta=beta,
+                                                stream=stream)
+    _, want = step()
+    torch.cuda.synchronize()
+    results, errors = [], []
+
+    def work():
+        try:
+            s = torch.cuda.Stream()
+            out = [step(s) for _ in range(20)]
+            s.synchronize()
+            results.extend(out)
+        except Exception as e:   # a thread's failure must reach the test
+            errors.append(e)
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors and len(results) == 40
+    for k, got in results:
+        assert torch.equal(k.codes, kept.codes) and torch.equal(k.scales, kept.scales)
+        for n, g in got.items():
+            a, b = g.double(), want[n].double()
+            room = 2 * R.half_step(gout.dtype) * b.abs() + 1e-5 * b.abs().max()
+            assert ((a - b).abs() <= room).all(), n
+            if key.startswith("depthwise"):
+                assert torch.equal(g, want[n]), n
+
+
+def test_a_given_stream():
+    x = make((1, 4, 40), torch.float32)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    k = dcn.dcn1d_checkpoint_pack(x, stream=s)
+    v = dcn.dcn1d_checkpoint_unpack(k, stream=s)
+    s.synchronize()
+    assert torch.equal(v, dcn.dcn1d_checkpoint_unpack(dcn.dcn1d_checkpoint_pack(x)))
