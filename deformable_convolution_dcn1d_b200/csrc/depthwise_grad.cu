@@ -181,7 +181,9 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
         const float be = a.q.beta ? ld_f32(static_cast<const T *>(a.q.beta) + c) : 0.0f;
         const bool affine = a.q.gamma || a.q.beta;
         const int8_t *codes = a.q.codes + row * L;
-        const uint8_t *scales = a.q.scales + row * a.nb;
+        // a checkpoint of L == 1 has its blocks along the channels
+        const uint8_t *scales = L == 1 ? a.q.scales + row / P.C_in * ck_blocks(P.C_in) + c / kCkBlock
+                                       : a.q.scales + row * a.nb;
         // gamma v + beta, each rounded; 1 v + 0 changes no value but the sign of a zero
         auto through = [&](float v) {
             if (a.q.gamma)
