@@ -75,6 +75,7 @@ int stage_bytes(const Problem &P) {
     return kGroup * P.K * (P.dtype == DCN1D_F32 ? 4 : 2) * (P.mask ? 2 : 1);
 }
 
+constexpr float kFarStart = 4194304.0f;  // 2^22, past every signal (fast_floor_ok)
 constexpr float kRound = 12582912.0f;    // 1.5 * 2^23: adding it rounds to an integer
 constexpr unsigned kRoundBits = 0x4B400000u;
 
@@ -275,26 +276,27 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
         constexpr int W = TWO ? 2 * K : K;                 // words of two positions' offsets
         uint32_t near_end = 0, o_next[W], m_next[MASK ? W : 1], g_next[TWO ? 2 : 1];
         auto two = [&](const T *from, uint32_t *to, int l, int per) {
-            // `per` values of positions l and l + 1 (kept inside the row)
+            // `per` values of positions l and l + 1; past the end of the row: zeros
+            const bool first = l < Lo, second = l + 1 < Lo;
             if (!TWO && a.even) {
                 const uint32_t *p = reinterpret_cast<const uint32_t *>(from + l * per);
 #pragma unroll
                 for (int k = 0; k < K; ++k)
                     if (k < per)
-                        to[k] = __ldg(p + k);
+                        to[k] = first ? __ldg(p + k) : 0u;
                 return;
             }
-            const int l1 = min(l + 1, Lo - 1);
 #pragma unroll
             for (int k = 0; k < 2 * K; ++k)
                 if (k < 2 * per) {
-                    const T *p = k < per ? from + l * per + k : from + l1 * per + k - per;
+                    const T *p = from + l * per + k;
+                    const bool in = k < per ? first : second;
                     if constexpr (TWO)
-                        to[k] = __ldg(reinterpret_cast<const uint32_t *>(p));
-                    else if (k % 2 == 0)
-                        to[k / 2] = __ldg(reinterpret_cast<const unsigned short *>(p));
-                    else
-                        to[k / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(p)) << 16;
+                        to[k] = in ? __ldg(reinterpret_cast<const uint32_t *>(p)) : 0u;
+                    else {
+                        const uint32_t v = in ? __ldg(reinterpret_cast<const unsigned short *>(p)) : 0u;
+                        to[k / 2] = k % 2 == 0 ? v : to[k / 2] | v << 16;
+                    }
                 }
         };
         // value i of those words
@@ -307,9 +309,7 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
                 return __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
         };
         auto fetch = [&](int l0) {
-            int l = l0 + 2 * me;
-            if (l >= Lo)                                   // an even position with two values
-                l = (Lo - 1) & ~1;
+            const int l = l0 + 2 * me;
             two(off, o_next, l, K);
             if (MASK)
                 two(mask, m_next, l, K);
@@ -335,10 +335,14 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
             float doff[2 * K], dmask[MASK ? 2 * K : 1];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const float g = l0 + 2 * me + u < Lo ? at(gg, u) : 0.0f;   // past the end: zeros
+                const float g = at(gg, u);
                 if (!AGAIN)
                     gb += g;
-                const float start = u ? start0 + (float)P.stride : start0;
+                // Taps past the end of the row are far from the signal: with their zeros they
+                // read zeros and add nothing, whatever x, the mask or the weight hold.
+                const float start = l0 + 2 * me + u >= Lo ? kFarStart
+                                    : u                   ? start0 + (float)P.stride
+                                                          : start0;
                 const float first = start + from_start, last = start + to_end;
                 int found[2 * K];
 #pragma unroll
