@@ -15,22 +15,25 @@
 // grad_x is added up in fixed point by integer atomics: shared memory has no native fp32
 // addition (a loop of compare-and-swap: 13 to 22 cycles a warp measured, more the more lanes
 // meet at a site, against about 3 for an integer one), and integers make the sum exact and
-// independent of the order.  With M the largest |m w grad_out| of the row (found first):
-//  * 16-bit types: multiples of M 2^-22 in one word.  The unit is 2^-13 of what one
-//    contribution of M 2^-9 rounds to in bf16.  A site may pass 2^31 only after more than
-//    256 contributions of M; every addition looks at what it found, and a row where one
-//    found 2^30 is added again in fp32.
-//  * fp32: two words, hi 2^-s + lo 2^-(s+B) with |hi| <= 2^A, |lo| <= 2^(B-1).  With N =
-//    L_out K < 2^n taps, A = 30 - n and B = 32 - n (at most 21 and 22) N additions overflow
-//    neither, wherever they meet; the unit is M 2^-30 at 2^16 taps.
-// A row whose M is not finite adds in fp32, so that NaN and infinities reach the sites they
-// belong to.
+// independent of the order.  Every site has a unit of its own, so that quiet stretches of a
+// row keep what fp32 additions would keep of them: a first walk takes the largest
+// contribution of each site (atomic maxima of the bits), and each site gets four bits q,
+// min(15, (E - e) / 4) for the row's largest exponent E and the site's e.  Its contributions
+// are whole multiples of 2^(E - 4q - 26), at most 2^-22 of the largest one and below 2^26 of
+// them: a contribution of at most 24 bits is off by at most 2^-23 of the site's largest,
+// against 2^-24 of the sum an fp32 addition.  (Sites whose largest is under 2^-60 of the
+// row's: by at most 2^-86 of that.)  A sum may pass 2^31 only after more than 16
+// contributions of the largest kind; every addition looks at what it found, and a row where
+// one found 2^30 is added again in fp32.  So is a row with a NaN or an infinity, so that
+// they reach the sites they belong to, and a row too long for the bits q beside its sums.
 //
-// Measured (B200): [8, 512, 16000] bf16, 3 taps, 450 us for 1.11 GB = 2.5 TB/s, 0.38 of the
-// copy bandwidth.  Bound by issue (84 % of the slots, 65 instructions a tap) and by the
-// shared-memory pipe (79 %: the two additions of a tap collide about 4 ways, as offsets
-// scatter the lanes).  Float atomics took 1194 us, two integers a sum 919, one position a
-// lane 542.  512 threads and at most 64 registers for K <= 4: two blocks an SM, so that one
+// Measured (B200): [8, 512, 16000] bf16, 3 taps, 768 us for 1.11 GB = 1.45 TB/s, 0.22 of the
+// copy bandwidth; fp32 1186 us.  Bound by issue (84 % of the slots, 112 instructions a tap,
+// about a third of them the first walk's) and by the shared-memory pipe (76 %: the two
+// additions or maxima of a tap collide about 4 ways, as offsets scatter the lanes).  One unit
+// for a whole row took 450 us and lost what lies far below the row's largest; fp32 additions
+// run at 61 SM cycles a warp and tap where these take 51 (rows of 34000 to 37000, bf16).
+// 512 threads and at most 64 registers for K <= 4: two blocks an SM, so that one
 // unpacks or writes out while the other walks; more taps need the registers.
 #include "checkpoint.cuh"
 #include "pairs.cuh"
@@ -49,9 +52,8 @@ struct Args {
     CheckpointConv q;
     float *part;                         // [B * C][K + 1]: grad_weight and grad_bias of a row
     int wpr;                             // warps of a row
-    int x_words, sum_words;              // 4-byte words of a row's x and of each sum's array
-    int a_bits, b_bits;                  // A and B above (16-bit types: A = 22)
-    bool fixed;                          // they leave a fine enough unit
+    int x_words, sum_words, code_words;  // 4-byte words of a row's x, its sums and the bits q
+    bool fixed;                          // sums in fixed point: there is room for the bits q
     bool wide;                           // offsets' gradients leave in 16-byte chunks
     bool even;                           // 16-bit types: two positions' values are whole words
     int64_t rows, nb;
@@ -63,24 +65,25 @@ template <class T> constexpr int lead() { return 16 / (int)sizeof(T) - 1; }
 int words_of(const Problem &P, int size) {
     return (((P.L_in + 3) * size + 16 - size + 15) / 16) * 4;
 }
-int sums_of(const Problem &P) { return P.dtype == DCN1D_F32 ? 2 : 1; }
-int row_words(const Problem &P) {
-    return words_of(P, P.dtype == DCN1D_F32 ? 4 : 2) + sums_of(P) * words_of(P, 4);
+int code_words_of(const Problem &P) { return (words_of(P, 4) + 31) / 32 * 4; }   // 8 sites a word
+int row_words(const Problem &P, bool fixed) {
+    return words_of(P, P.dtype == DCN1D_F32 ? 4 : 2) + words_of(P, 4) + (fixed ? code_words_of(P) : 0);
 }
 
 constexpr int kGroup = 64;               // positions of a warp's step, two neighbours a lane
 
-// Staging of a group's gradients of offsets (and mask).
-int stage_bytes(const Problem &P) {
-    return kGroup * P.K * (P.dtype == DCN1D_F32 ? 4 : 2) * (P.mask ? 2 : 1);
-}
+// Staging of a group's gradients of offsets, then of the mask.
+int stage_bytes(const Problem &P) { return kGroup * P.K * (P.dtype == DCN1D_F32 ? 4 : 2); }
 
 constexpr float kFarStart = 4194304.0f;  // 2^22, past every signal (fast_floor_ok)
-constexpr float kRound = 12582912.0f;    // 1.5 * 2^23: adding it rounds to an integer
-constexpr unsigned kRoundBits = 0x4B400000u;
+constexpr int kBits = 26;                // of a site's largest contribution, in its units
+// The least exponent (biased) of a row's largest contribution at which every unit is a normal
+// number.  Rows below are taken times 2^100 (and at least this), sums and all.
+constexpr int kLeastTop = kBits + 60;
+constexpr float kUp = 0x1p100f, kDown = 0x1p-100f;
 
-// 2^e as a float, -126 <= e <= 127.
-__device__ __forceinline__ float two_to(int e) { return __uint_as_float((unsigned)(e + 127) << 23); }
+// What a walk over a row's taps does with grad_x; the first and the last write nothing else.
+enum Walk { TOPS, FIXED, FLOAT, AGAIN };
 
 // The `n` staged values of a group (fewer at the row's end) to global memory.
 template <class T, int K>
@@ -98,57 +101,14 @@ __device__ __forceinline__ void unstage(const T *from, T *to, int n, bool wide) 
     }
 }
 
-// Largest |value| of v[0 .. n) over the lanes of a row, as the bits of a float of its type
-// (NaN above infinity above all others), a lane's part.
-template <class T>
-__device__ __forceinline__ uint32_t top_bits(const T *v, int64_t n, int lane, int lanes) {
-    constexpr int VE = 16 / (int)sizeof(T);
-    uint32_t top = 0;
-    int64_t i = lane;
-    if ((reinterpret_cast<uintptr_t>(v) & 15) == 0) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(v);
-#pragma unroll 2
-        for (int64_t c = lane; c < n / VE; c += lanes) {
-            const uint4 u = __ldg(p + c);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (sizeof(T) == 4)
-                    top = max(top, w[j] & 0x7FFFFFFFu);
-                else
-                    top = __vmaxu2(top, w[j] & 0x7FFF7FFFu);
-            }
-        }
-        i += n / VE * VE;
-    }
-    if constexpr (sizeof(T) == 2)
-        top = max(top >> 16, top & 0xFFFFu);
-    for (; i < n; i += lanes) {
-        if constexpr (sizeof(T) == 4)
-            top = max(top, reinterpret_cast<const uint32_t *>(v)[i] & 0x7FFFFFFFu);
-        else
-            top = max(top, (uint32_t)(reinterpret_cast<const unsigned short *>(v)[i] & 0x7FFF));
-    }
-    return top;
-}
-
-template <class T>
-__device__ __forceinline__ float bits_to_f32(uint32_t b) {
-    if constexpr (sizeof(T) == 4)
-        return __uint_as_float(b);
-    else if constexpr (std::is_same<T, __half>::value)
-        return __half2float(__ushort_as_half((unsigned short)b));
-    else
-        return __uint_as_float(b << 16);
-}
-
 // Block of blockDim.x / 32 warps, wpr of them a row.  ALL: every gradient is wanted.
 template <class T, int K, bool MASK, bool ALL>
-__global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(const Args a) {
-    constexpr bool TWO = sizeof(T) == 4;                   // two words a sum
+__global__ void __launch_bounds__(512, K <= (sizeof(T) == 4 ? 3 : 4) ? 2 : 1)
+    depthwise_grad_kernel(const Args a) {
+    constexpr bool F32 = sizeof(T) == 4;
     extern __shared__ uint4 raw4[];
     __shared__ float sums[kMaxWarps][kMaxK + 1];
-    __shared__ uint32_t tops[kMaxWarps][2];
+    __shared__ uint32_t tops[kMaxWarps];
     __shared__ int over[kMaxWarps];
     const Problem &P = a.q.P;
     const BackwardGrads &G = a.q.G;
@@ -161,12 +121,13 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
     const int L = P.L_in, Lo = P.L_out;
     const bool want_x = ALL || G.x, want_off = ALL || G.off, want_mask = MASK && (ALL || G.mask);
     // site s stands for position s - 1
-    const int words = a.x_words + (TWO ? 2 : 1) * a.sum_words;
+    const int words = a.x_words + a.sum_words + a.code_words;
     uint32_t *base = reinterpret_cast<uint32_t *>(raw4) + (size_t)mine * words;
     T *xs = reinterpret_cast<T *>(base) + lead<T>();
-    int *hi = reinterpret_cast<int *>(base + a.x_words) + 3, *lo = hi + a.sum_words;   // lo: TWO
+    int *sum = reinterpret_cast<int *>(base + a.x_words) + 3;
+    uint32_t *qs = base + a.x_words + a.sum_words;         // q of sites 8 i - 3 .. 8 i + 4 in word i
     T *stage = reinterpret_cast<T *>(reinterpret_cast<uint32_t *>(raw4) + (size_t)rpb * words) +
-               warp * kGroup * K * (MASK ? 2 : 1);
+               warp * kGroup * K;
     const int c = live ? (int)(row % P.C_in) : 0;
     const int64_t out0 = row * Lo;
     const T *gout = static_cast<const T *>(G.gout) + out0;
@@ -174,7 +135,7 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
     float w[K];
     auto clear = [&]() {
         uint4 *p = reinterpret_cast<uint4 *>(base + a.x_words);
-        for (int i = lane; i < (TWO ? 2 : 1) * a.sum_words / 4; i += lanes)
+        for (int i = lane; i < a.sum_words / 4; i += lanes)
             p[i] = make_uint4(0, 0, 0, 0);
     };
     if (live) {
@@ -225,40 +186,10 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
 #pragma unroll
         for (int k = 0; k < K; ++k)
             w[k] = ld_f32(static_cast<const T *>(P.w) + c * K + k);
-        if (want_x) {
-            const uint32_t tg = top_bits(gout, Lo, lane, lanes);
-            const uint32_t tm = MASK ? top_bits(mask, (int64_t)Lo * K, lane, lanes) : 0u;
-            const uint32_t wg = __reduce_max_sync(0xFFFFFFFFu, tg), wm = __reduce_max_sync(0xFFFFFFFFu, tm);
-            if (me == 0) {
-                tops[warp][0] = wg;
-                tops[warp][1] = wm;
-                over[warp] = 0;
-            }
-        }
+        if (me == 0)
+            over[warp] = 0;
     }
     __syncthreads();
-    float to_hi = 0.0f;                                    // 2^s
-    int s = 0;
-    bool fixed = true;
-    if (live && want_x) {
-        uint32_t bg = 0, bm = 0;
-        for (int i = 0; i < a.wpr; ++i) {
-            bg = max(bg, tops[mine * a.wpr + i][0]);
-            bm = max(bm, tops[mine * a.wpr + i][1]);
-        }
-        float tw = 0.0f;
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            tw = w[k] == w[k] ? fmaxf(tw, fabsf(w[k])) : INFINITY;
-        // M < 2^e; the product, associated as the contributions are, may round down twice
-        const float tg = bits_to_f32<T>(bg), tm = MASK ? bits_to_f32<T>(bm) : 1.0f;
-        const float M = tw * tg * tm;
-        fixed = a.fixed && M < INFINITY && tg < INFINITY && tm < INFINITY && tw < INFINITY;   // not for NaN
-        const int e = (int)((__float_as_uint(M) + 2u) >> 23) - 126;
-        s = max(-126, min(126, a.a_bits - e));
-        to_hi = two_to(s);
-    }
-    const float to_lo = two_to(a.b_bits);
     float gw[K], gb = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -269,16 +200,18 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
     const T *off = static_cast<const T *>(P.off) + out0 * K;
     T *goff = static_cast<T *>(G.off) + (G.off ? out0 * K : 0);
     T *gmask = static_cast<T *>(G.mask) + (G.mask ? out0 * K : 0);
-    // All taps of the row.  FIXED: grad_x in fixed point, and whether a site came near the
-    // end of its range; AGAIN: grad_x alone, the rest has been written.
-    auto walk = [&](auto fixed_tag, auto again_tag) {
-        constexpr bool FIXED = decltype(fixed_tag)::value, AGAIN = decltype(again_tag)::value;
-        constexpr int W = TWO ? 2 * K : K;                 // words of two positions' offsets
-        uint32_t near_end = 0, o_next[W], m_next[MASK ? W : 1], g_next[TWO ? 2 : 1];
+    uint32_t unit_bits = 0;                                // 1 / the unit of q = 0, as a float
+    float up = 1.0f;                                       // kUp in rows of tiny contributions
+    // All taps of the row.  FIXED returns whether a site came near the end of its range.
+    auto walk = [&](auto mode) {
+        constexpr Walk MODE = decltype(mode)::value;
+        constexpr bool REST = MODE == FIXED || MODE == FLOAT;   // all gradients, not grad_x alone
+        constexpr int W = F32 ? 2 * K : K;                 // words of two positions' offsets
+        uint32_t near_end = 0, o_next[W], m_next[MASK ? W : 1], g_next[F32 ? 2 : 1];
         auto two = [&](const T *from, uint32_t *to, int l, int per) {
             // `per` values of positions l and l + 1; past the end of the row: zeros
             const bool first = l < Lo, second = l + 1 < Lo;
-            if (!TWO && a.even) {
+            if (!F32 && a.even) {
                 const uint32_t *p = reinterpret_cast<const uint32_t *>(from + l * per);
 #pragma unroll
                 for (int k = 0; k < K; ++k)
@@ -291,7 +224,7 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
                 if (k < 2 * per) {
                     const T *p = from + l * per + k;
                     const bool in = k < per ? first : second;
-                    if constexpr (TWO)
+                    if constexpr (F32)
                         to[k] = in ? __ldg(reinterpret_cast<const uint32_t *>(p)) : 0u;
                     else {
                         const uint32_t v = in ? __ldg(reinterpret_cast<const unsigned short *>(p)) : 0u;
@@ -301,7 +234,7 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
         };
         // value i of those words
         auto at = [](const uint32_t *w, int i) -> float {
-            if constexpr (TWO)
+            if constexpr (F32)
                 return __uint_as_float(w[i]);
             else if constexpr (std::is_same<T, __half>::value)
                 return __half2float(__ushort_as_half((unsigned short)(i % 2 ? w[i / 2] >> 16 : w[i / 2])));
@@ -319,7 +252,7 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
         if (l0 < Lo)
             fetch(l0);
         for (; l0 < Lo; l0 += 2 * lanes) {
-            uint32_t o[W], m[MASK ? W : 1], gg[TWO ? 2 : 1];
+            uint32_t o[W], m[MASK ? W : 1], gg[F32 ? 2 : 1];
 #pragma unroll
             for (int k = 0; k < W; ++k) {
                 o[k] = o_next[k];
@@ -327,8 +260,8 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
                     m[k] = m_next[k];
             }
             gg[0] = g_next[0];
-            if (TWO)
-                gg[TWO ? 1 : 0] = g_next[TWO ? 1 : 0];
+            if (F32)
+                gg[F32 ? 1 : 0] = g_next[F32 ? 1 : 0];
             if (l0 + 2 * lanes < Lo)
                 fetch(l0 + 2 * lanes);
             const float start0 = (float)((l0 + 2 * me) * P.stride - P.padding);
@@ -336,7 +269,7 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const float g = at(gg, u);
-                if (!AGAIN)
+                if (REST)
                     gb += g;
                 // Taps past the end of the row are far from the signal: with their zeros they
                 // read zeros and add nothing, whatever x, the mask or the weight hold.
@@ -357,7 +290,7 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
                         min(__float_as_uint(t) - (kFloorMagicBits - 1u), (uint32_t)L + 1u);
                     const float mk = MASK ? at(m, u * K + k) : 1.0f;
                     const float dv = w[k] * g, mdv = MASK ? mk * dv : dv;
-                    if (!AGAIN) {
+                    if (REST) {
                         const float x0 = to_f32(xs[site]), x1 = to_f32(xs[site + 1]);
                         const float slope = x1 - x0, v = fmaf(f, slope, x0);
                         gw[k] = fmaf(MASK ? mk * g : g, v, gw[k]);
@@ -368,27 +301,25 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
                     }
                     if (want_x) {
                         const float d = site <= (uint32_t)L ? mdv : 0.0f;   // far taps add zeros
-                        const float c1 = f * d, c0 = d - c1;
-                        if constexpr (FIXED) {
-                            const float h0 = fmaf(c0, to_hi, kRound), h1 = fmaf(c1, to_hi, kRound);
-                            found[2 * k] = atomicAdd(hi + site, (int)(__float_as_uint(h0) - kRoundBits));
-                            found[2 * k + 1] =
-                                atomicAdd(hi + site + 1, (int)(__float_as_uint(h1) - kRoundBits));
-                            if constexpr (TWO) {
-                                const float r0 = fmaf(c0, to_hi, kRound - h0),
-                                            r1 = fmaf(c1, to_hi, kRound - h1);
-                                atomicAdd(lo + site,
-                                          (int)(__float_as_uint(fmaf(r0, to_lo, kRound)) - kRoundBits));
-                                atomicAdd(lo + site + 1,
-                                          (int)(__float_as_uint(fmaf(r1, to_lo, kRound)) - kRoundBits));
-                            }
+                        const float du = MODE == FIXED ? __fmul_rn(d, up) : d;
+                        const float c1 = __fmul_rn(f, du), c0 = __fsub_rn(du, c1);
+                        if constexpr (MODE == TOPS) {
+                            atomicMax(sum + site, (int)(__float_as_uint(c0) & 0x7FFFFFFFu));
+                            atomicMax(sum + site + 1, (int)(__float_as_uint(c1) & 0x7FFFFFFFu));
+                        } else if constexpr (MODE == FIXED) {
+                            auto in_units = [&](float c, uint32_t slot) {
+                                const uint32_t q = qs[slot >> 3] >> (slot * 4 & 31u) & 15u;
+                                return __float2int_rn(__fmul_rn(c, __uint_as_float(unit_bits + (q << 25))));
+                            };
+                            found[2 * k] = atomicAdd(sum + site, in_units(c0, site + 3));
+                            found[2 * k + 1] = atomicAdd(sum + site + 1, in_units(c1, site + 4));
                         } else {
-                            atomicAdd(reinterpret_cast<float *>(hi) + site, c0);
-                            atomicAdd(reinterpret_cast<float *>(hi) + site + 1, c1);
+                            atomicAdd(reinterpret_cast<float *>(sum) + site, c0);
+                            atomicAdd(reinterpret_cast<float *>(sum) + site + 1, c1);
                         }
                     }
                 }
-                if constexpr (FIXED && !TWO) {
+                if constexpr (MODE == FIXED) {
                     if (want_x) {
 #pragma unroll
                         for (int k = 0; k < 2 * K; ++k)    // bit 31: 2^30 or more, either sign
@@ -396,11 +327,11 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
                     }
                 }
             }
-            if constexpr (AGAIN)
+            if constexpr (!REST)
                 continue;
             const int n = min(kGroup, Lo - l0) * K;
             auto put = [&](T *to, const float (&d)[2 * K]) {
-                if constexpr (TWO) {
+                if constexpr (F32) {
 #pragma unroll
                     for (int k = 0; k < 2 * K; ++k)
                         to[2 * K * me + k] = from_f32<T>(d[k]);
@@ -412,62 +343,107 @@ __global__ void __launch_bounds__(512, K <= 4 ? 2 : 1) depthwise_grad_kernel(con
                     }
                 }
             };
-            if (want_off)
+            if (want_off) {
                 put(stage, doff);
-            if constexpr (MASK)
-                if (want_mask)
-                    put(stage + kGroup * K, dmask);
-            __syncwarp();
-            if (want_off)
+                __syncwarp();
                 unstage<T, K>(stage, goff + l0 * K, n, a.wide);
-            if (want_mask)
-                unstage<T, K>(stage + kGroup * K, gmask + l0 * K, n, a.wide);
-            __syncwarp();
+                __syncwarp();
+            }
+            if constexpr (MASK)
+                if (want_mask) {
+                    put(stage, dmask);
+                    __syncwarp();
+                    unstage<T, K>(stage, gmask + l0 * K, n, a.wide);
+                    __syncwarp();
+                }
         }
         return near_end >> 31;
     };
+    bool fixed = false;
+    int top = 0;
+    if (want_x && a.fixed) {                               // the same in every thread of the grid
+        if (live)
+            walk(std::integral_constant<Walk, TOPS>());
+        __syncthreads();
+        // the bits of the row's largest contribution (NaN above infinity above all others)
+        uint4 *tp = reinterpret_cast<uint4 *>(base + a.x_words);
+        uint32_t t = 0;
+        if (live)
+            for (int i = lane; i < a.sum_words / 4; i += lanes)
+                t = max(t, max(max(tp[i].x, tp[i].y), max(tp[i].z, tp[i].w)));
+        t = __reduce_max_sync(0xFFFFFFFFu, t);
+        if (me == 0)
+            tops[warp] = t;
+        __syncthreads();
+        t = 0;
+        for (int i = 0; i < a.wpr; ++i)
+            t = max(t, tops[mine * a.wpr + i]);
+        fixed = t < 0x7F800000u;
+        if ((int)(t >> 23) < kLeastTop)
+            up = kUp;
+        top = max((int)(__float_as_uint(__uint_as_float(t) * up) >> 23), kLeastTop);
+        unit_bits = (uint32_t)(253 + kBits - top) << 23;
+        if (live)
+            for (int i = lane; i < a.code_words; i += lanes) {
+                uint32_t q = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (2 * i + h < a.sum_words / 4) {
+                        const uint4 u = tp[2 * i + h];
+                        const uint32_t e[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int at = (int)(__float_as_uint(__uint_as_float(e[j]) * up) >> 23);
+                            q |= (uint32_t)max(0, min(15, (top - at) >> 2)) << (16 * h + 4 * j);
+                        }
+                        tp[2 * i + h] = make_uint4(0, 0, 0, 0);
+                    }
+                qs[i] = q;
+            }
+        __syncthreads();
+    }
     if (live) {
         if (fixed) {
-            if (walk(std::true_type(), std::false_type()))
+            if (walk(std::integral_constant<Walk, FIXED>()))
                 over[mine * a.wpr] = 1;
         } else {
-            walk(std::false_type(), std::false_type());
+            walk(std::integral_constant<Walk, FLOAT>());
         }
     }
-    if constexpr (!TWO) {
+    if (want_x && a.fixed) {
         __syncthreads();
-        const bool redo = live && want_x && fixed && over[mine * a.wpr];
+        const bool redo = live && fixed && over[mine * a.wpr];
         if (__syncthreads_or(redo)) {
             if (redo)
                 clear();
             __syncthreads();
             if (redo) {
                 fixed = false;
-                walk(std::false_type(), std::true_type());
+                walk(std::integral_constant<Walk, AGAIN>());
             }
         }
     }
     __syncthreads();
     if (live && want_x) {
         T *gx = static_cast<T *>(G.x) + row * L;
-        const float from_hi = two_to(-s), from_lo = two_to(-a.b_bits);
-        auto value = [&](int i) {
-            const int h = hi[i + 1];
-            if (!fixed)
-                return __int_as_float(h);
-            return (TWO ? fmaf((float)lo[i + 1], from_lo, (float)h) : (float)h) * from_hi;
+        const uint32_t from_bits = (uint32_t)(top + 1 - kBits) << 23;   // the unit of q = 0
+        const float down = up == 1.0f ? 1.0f : kDown;
+        auto value = [&](int v, uint32_t q) {              // from a word of sums
+            return fixed ? (float)v * __uint_as_float(from_bits - ((q & 15u) << 25)) * down
+                         : __int_as_float(v);
         };
+        auto q_of = [&](int slot) { return fixed ? qs[slot >> 3] >> (slot * 4 & 31) : 0u; };
         if (sizeof(T) == 2 && L % 4 == 0 && (reinterpret_cast<uintptr_t>(G.x) & 7) == 0) {
             for (int i = lane * 4; i < L; i += lanes * 4) {
-                const int4 h = *reinterpret_cast<const int4 *>(hi + 1 + i);
-                auto one = [&](int v) { return fixed ? (float)v * from_hi : __int_as_float(v); };
-                const T four[4] = {from_f32<T>(one(h.x)), from_f32<T>(one(h.y)), from_f32<T>(one(h.z)),
-                                   from_f32<T>(one(h.w))};
+                const int4 v = *reinterpret_cast<const int4 *>(sum + 1 + i);
+                const uint32_t q = q_of(i + 4);            // four positions' are in one word
+                const T four[4] = {from_f32<T>(value(v.x, q)), from_f32<T>(value(v.y, q >> 4)),
+                                   from_f32<T>(value(v.z, q >> 8)), from_f32<T>(value(v.w, q >> 12))};
                 __stcs(reinterpret_cast<uint2 *>(gx + i), *reinterpret_cast<const uint2 *>(four));
             }
         } else {
             for (int i = lane; i < L; i += lanes)
-                gx[i] = from_f32<T>(value(i));
+                gx[i] = from_f32<T>(value(sum[i + 1], q_of(i + 4)));
         }
     }
     if (!a.part)
@@ -510,8 +486,8 @@ __global__ void __launch_bounds__(256) depthwise_weight_grad_kernel(const float 
 }
 
 // Dynamic shared memory of a block of rpb rows of wpr warps.
-size_t block_bytes(const Problem &P, int wpr, int rpb) {
-    return (size_t)rpb * row_words(P) * 4 + (size_t)rpb * wpr * stage_bytes(P);
+size_t block_bytes(const Problem &P, int wpr, int rpb, bool fixed) {
+    return (size_t)rpb * row_words(P, fixed) * 4 + (size_t)rpb * wpr * stage_bytes(P);
 }
 
 template <class T, int K>
@@ -525,12 +501,6 @@ cudaError_t run(const CheckpointConv &q, void *ws, cudaStream_t s, int *launches
     a.nb = ck_blocks(P.L_in);
     a.x_words = words_of(P, sizeof(T));
     a.sum_words = words_of(P, 4);
-    int n = 0;                                             // N < 2^n
-    while ((1LL << n) <= (int64_t)P.L_out * K)
-        ++n;
-    a.a_bits = sizeof(T) == 2 ? 22 : 30 - n < 21 ? 30 - n : 21;
-    a.b_bits = 32 - n < 22 ? 32 - n : 22;
-    a.fixed = sizeof(T) == 2 || n <= 18;
     const int es = P.dtype == DCN1D_F32 ? 4 : 2;
     a.wide = (int64_t)P.L_out * K % (16 / es) == 0 &&
              ((reinterpret_cast<uintptr_t>(G.off) | reinterpret_cast<uintptr_t>(G.mask)) & 15) == 0;
@@ -539,13 +509,15 @@ cudaError_t run(const CheckpointConv &q, void *ws, cudaStream_t s, int *launches
     // a warp for each 64 positions, up to the block; then as many rows as make a block of
     // 8 warps
     const int longest = P.L_out > P.L_in ? P.L_out : P.L_in;
+    a.fixed = block_bytes(P, 1, 1, true) <= kSmem;
+    a.code_words = a.fixed ? code_words_of(P) : 0;
     a.wpr = 1;
-    while (a.wpr < kMaxWarps && a.wpr * 64 < longest && block_bytes(P, 2 * a.wpr, 1) <= kSmem)
+    while (a.wpr < kMaxWarps && a.wpr * 64 < longest && block_bytes(P, 2 * a.wpr, 1, a.fixed) <= kSmem)
         a.wpr *= 2;
     int rpb = a.wpr < 8 ? 8 / a.wpr : 1;
-    while (rpb > 1 && block_bytes(P, a.wpr, rpb) > 48 * 1024)
+    while (rpb > 1 && block_bytes(P, a.wpr, rpb, a.fixed) > 48 * 1024)
         rpb /= 2;
-    const size_t shared = block_bytes(P, a.wpr, rpb);
+    const size_t shared = block_bytes(P, a.wpr, rpb, a.fixed);
     const bool all = G.x && G.off && (!P.mask || G.mask);
     auto kernel = P.mask ? (all ? depthwise_grad_kernel<T, K, true, true>
                                 : depthwise_grad_kernel<T, K, true, false>)
@@ -584,7 +556,7 @@ cudaError_t run_k(const CheckpointConv &q, void *ws, cudaStream_t s, int *launch
 
 bool depthwise_grad_supported(const Problem &P) {
     return P.groups == P.C_in && P.C_out == P.C_in && P.offset_groups == P.C_in && P.K <= kMaxK &&
-           P.B > 0 && block_bytes(P, 1, 1) <= kSmem && fast_floor_ok(P);
+           P.B > 0 && block_bytes(P, 1, 1, false) <= kSmem && fast_floor_ok(P);
 }
 
 size_t depthwise_grad_workspace(const Problem &P, const BackwardGrads &G) {

@@ -509,13 +509,14 @@ int dcn1d_checkpoint_unpack(const dcn1d_tensor *codes, const dcn1d_tensor *scale
  * dcn1d_backward_checkpoint_workspace_size gives.
  *
  * The depthwise layer with offsets of each channel's own (groups == offset_groups == C_in ==
- * C_out, K <= 9, L_in up to about 18000 in F32 and 37000 in 16-bit types) runs as one kernel
+ * C_out, K <= 9, L_in up to about 28000 in F32 and 38000 in 16-bit types) runs as one kernel
  * that reads the checkpoint itself, and a small one that joins the batch for grad_weight and
  * grad_bias; every sum then has an order-independent value or a fixed order.  Its grad_x is
- * added in fixed point: with M the largest |mask * weight * grad_out| of a row (b, c), in
- * multiples of M 2^-22 (16-bit types) or M 2^-26 and finer (F32); rows of more than 2^18 taps
- * in F32, rows where hundreds of contributions near M meet at one position in 16-bit types,
- * and rows with a NaN or an infinity add in fp32 (low bits may then differ between calls).
+ * added in fixed point, each position in units of its own: a contribution is off by at most
+ * 2^-23 of the largest one at its position (2^-86 of the row's largest where that is more).
+ * Rows where more than 16 contributions of the largest kind meet at one position, rows with a
+ * NaN or an infinity and rows past about 26000 (F32) or 35000 (16-bit types) add in fp32; low
+ * bits may then differ between calls.
  * Other layers unpack the checkpoint into the workspace and run dcn1d_backward_lr's kernels.
  */
 int64_t dcn1d_backward_checkpoint_workspace_size(
