@@ -54,6 +54,7 @@ struct Args {
     int wpr;                             // warps of a row
     int x_words, sum_words, code_words;  // 4-byte words of a row's x, its sums and the bits q
     bool fixed;                          // sums in fixed point: there is room for the bits q
+    bool staged;                         // offsets' gradients go through shared memory
     bool wide;                           // offsets' gradients leave in 16-byte chunks
     bool even;                           // 16-bit types: two positions' values are whole words
     int64_t rows, nb;
@@ -343,19 +344,31 @@ __global__ void __launch_bounds__(512, K <= (sizeof(T) == 4 ? 3 : 4) ? 2 : 1)
                     }
                 }
             };
-            if (want_off) {
-                put(stage, doff);
-                __syncwarp();
-                unstage<T, K>(stage, goff + l0 * K, n, a.wide);
-                __syncwarp();
-            }
-            if constexpr (MASK)
-                if (want_mask) {
-                    put(stage, dmask);
+            if (a.staged) {
+                if (want_off) {
+                    put(stage, doff);
                     __syncwarp();
-                    unstage<T, K>(stage, gmask + l0 * K, n, a.wide);
+                    unstage<T, K>(stage, goff + l0 * K, n, a.wide);
                     __syncwarp();
                 }
+                if constexpr (MASK)
+                    if (want_mask) {
+                        put(stage, dmask);
+                        __syncwarp();
+                        unstage<T, K>(stage, gmask + l0 * K, n, a.wide);
+                        __syncwarp();
+                    }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2 * K; ++k) {
+                    const int i = 2 * K * me + k;
+                    if (want_off && i < n)
+                        goff[l0 * K + i] = from_f32<T>(doff[k]);
+                    if constexpr (MASK)
+                        if (want_mask && i < n)
+                            gmask[l0 * K + i] = from_f32<T>(dmask[k]);
+                }
+            }
         }
         return near_end >> 31;
     };
@@ -486,8 +499,8 @@ __global__ void __launch_bounds__(256) depthwise_weight_grad_kernel(const float 
 }
 
 // Dynamic shared memory of a block of rpb rows of wpr warps.
-size_t block_bytes(const Problem &P, int wpr, int rpb, bool fixed) {
-    return (size_t)rpb * row_words(P, fixed) * 4 + (size_t)rpb * wpr * stage_bytes(P);
+size_t block_bytes(const Problem &P, int wpr, int rpb, bool fixed, bool staged) {
+    return (size_t)rpb * row_words(P, fixed) * 4 + (staged ? (size_t)rpb * wpr * stage_bytes(P) : 0);
 }
 
 template <class T, int K>
@@ -509,15 +522,19 @@ cudaError_t run(const CheckpointConv &q, void *ws, cudaStream_t s, int *launches
     // a warp for each 64 positions, up to the block; then as many rows as make a block of
     // 8 warps
     const int longest = P.L_out > P.L_in ? P.L_out : P.L_in;
-    a.fixed = block_bytes(P, 1, 1, true) <= kSmem;
-    a.code_words = a.fixed ? code_words_of(P) : 0;
     a.wpr = 1;
-    while (a.wpr < kMaxWarps && a.wpr * 64 < longest && block_bytes(P, 2 * a.wpr, 1, a.fixed) <= kSmem)
+    while (a.wpr < kMaxWarps && a.wpr * 64 < longest)
         a.wpr *= 2;
+    // Rows near the limit give up the staging, and at last the bits q, before they give up
+    // warps: [2, 148, 17900] fp32, 9 taps with a mask, takes 375 us, and took 978 with the few
+    // warps that its staging left room for.
+    a.fixed = block_bytes(P, a.wpr, 1, true, false) <= kSmem;
+    a.staged = block_bytes(P, a.wpr, 1, a.fixed, true) <= kSmem;
+    a.code_words = a.fixed ? code_words_of(P) : 0;
     int rpb = a.wpr < 8 ? 8 / a.wpr : 1;
-    while (rpb > 1 && block_bytes(P, a.wpr, rpb, a.fixed) > 48 * 1024)
+    while (rpb > 1 && block_bytes(P, a.wpr, rpb, a.fixed, a.staged) > 48 * 1024)
         rpb /= 2;
-    const size_t shared = block_bytes(P, a.wpr, rpb, a.fixed);
+    const size_t shared = block_bytes(P, a.wpr, rpb, a.fixed, a.staged);
     const bool all = G.x && G.off && (!P.mask || G.mask);
     auto kernel = P.mask ? (all ? depthwise_grad_kernel<T, K, true, true>
                                 : depthwise_grad_kernel<T, K, true, false>)
@@ -556,7 +573,7 @@ cudaError_t run_k(const CheckpointConv &q, void *ws, cudaStream_t s, int *launch
 
 bool depthwise_grad_supported(const Problem &P) {
     return P.groups == P.C_in && P.C_out == P.C_in && P.offset_groups == P.C_in && P.K <= kMaxK &&
-           P.B > 0 && block_bytes(P, 1, 1, false) <= kSmem && fast_floor_ok(P);
+           P.B > 0 && block_bytes(P, 1, 1, false, false) <= kSmem && fast_floor_ok(P);
 }
 
 size_t depthwise_grad_workspace(const Problem &P, const BackwardGrads &G) {

@@ -6,6 +6,7 @@ import torch
 
 import depthwise_ref as D
 import deformable_convolution_dcn1d_b200 as dcn
+from gpu_util import TOL, norm_err
 
 pytestmark = pytest.mark.gpu
 
@@ -169,3 +170,20 @@ def test_equal_calls_give_equal_bits(L, K, dt, mask):
         _, again = run(t, 1, K // 2, 1, True, kept=kept)
         for n in first:
             assert torch.equal(first[n], again[n]), n
+
+
+# rows around the ends of what shared memory holds: with the staged stores, without them, and
+# without the sites' own units (fp32 additions)
+@pytest.mark.parametrize("L,K,dt,mask", [
+    (34000, 2, "bf16", False), (34900, 9, "f16", True), (37500, 3, "bf16", True), (38600, 2, "bf16", False),
+    (22000, 9, "f32", True), (26500, 3, "f32", False), (28000, 2, "f32", True), (29000, 2, "f32", False)])
+def test_rows_near_the_limit(L, K, dt, mask):
+    t = make(TYPES[dt], 1, 3, L, K, 1, K // 2, 1, mask, spread=2.0)
+    if L in (38600, 29000):     # past the limit: the checkpoint is unpacked, other kernels run
+        _, got = run(t, 1, K // 2, 1, True)
+        x = dcn.dcn1d_checkpoint_unpack(dcn.dcn1d_checkpoint_pack(t["x"]), dtype=TYPES[dt])
+        ref = D.backward(x, t["off"], t["mask"], t["w"], t["gout"], 1, K // 2, 1, True)[0]
+        for n, g in got.items():
+            assert norm_err(g.double().cpu().numpy(), ref[n].cpu().numpy()) <= TOL[dt], n
+        return
+    check(t, 1, K // 2, 1, True)
