@@ -21,7 +21,11 @@
 // k)^2, a k for each warp, and joins groups of n_i values about a common k by
 //   s1 = sum_i s1_i + n_i d_i,  s2 = sum_i s2_i + 2 d_i s1_i + n_i d_i^2,  d_i = k_i - k:
 // one exchange instead of one for the mean and one for the variance, and no difference of
-// large squares however far the mean is from zero (s1 carries what rounding k lost).
+// large squares however far the mean is from zero (s1 carries what rounding k lost).  Where
+// a few large channels put k far from the mean, s2 still cancels; a position at which the
+// groups' s2 add up to more than three times what is left takes its sums again about the
+// mean just found.  Rounding then costs the variance at most three times what it costs the
+// sum of squares about the mean, everywhere, and ordinary values are walked once.
 #include <cooperative_groups.h>
 
 #include "checkpoint.cuh"
@@ -246,9 +250,9 @@ __device__ __forceinline__ float sum8(float v) {
     return v;
 }
 
-// Sums of a group of n values about k.
+// Sums of a group of n values about k; raw: the s2 of the groups it was joined from.
 struct Moments {
-    float k, s1, s2;
+    float k, s1, s2, raw;
 };
 
 // A group of n values a lane of eight (n may be 0, but not in the first lane), joined about
@@ -259,7 +263,8 @@ __device__ __forceinline__ Moments join8(Moments m, float n) {
     const float all = sum8(n), k = k0 + sum8(some ? fmaf(n, m.k - k0, m.s1) : 0.0f) / fmaxf(all, 1.0f);
     const float d = m.k - k;
     return Moments{k, sum8(some ? fmaf(n, d, m.s1) : 0.0f),
-                   sum8(some ? fmaf(d, fmaf(n, d, 2.0f * m.s1), m.s2) : 0.0f)};
+                   sum8(some ? fmaf(d, fmaf(n, d, 2.0f * m.s1), m.s2) : 0.0f),
+                   sum8(some ? m.raw : 0.0f)};
 }
 
 // A walk of the clusters of a launch over the tiles.
@@ -292,9 +297,11 @@ __device__ __forceinline__ float warp_rows(const P &p, int nrow) {
     return (float)n;
 }
 
-// (-mean, rstd) of C values from their sums, NaN kept (fmaxf drops it).
-__device__ __forceinline__ float2 finish(const Moments &m, const Tiling &t, float eps) {
+// (-mean, rstd) of C values from their sums, NaN kept (fmaxf drops it), and whether the
+// variance cancelled too far (never for NaN and infinities).
+__device__ __forceinline__ float2 finish(const Moments &m, const Tiling &t, float eps, bool *far) {
     const float off = m.s1 * t.inv_c, var = fmaxf(m.s2 * t.inv_c - off * off, 0.0f);
+    *far = m.raw * t.inv_c > 3.0f * (var + eps) && m.raw < INFINITY && m.s2 == m.s2;
     return make_float2(-(m.k + off), 1.0f / sqrtf((m.s2 == m.s2 ? var : m.s2) + eps));
 }
 
@@ -365,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_tile_kernel(const NormProble
     if (p.lane == 0)
         count[threadIdx.x / 32] = rows;
     int turn = 0;
+    bool far = false;                          // this thread's position takes its sums again
     for (; w.b < P.B; w.step(t), turn ^= 1) {
         const int64_t l0 = (int64_t)w.lt << t.tw_log;
         const int64_t left = P.L - l0;         // positions of this tile (tw or more: all)
@@ -388,33 +396,38 @@ __global__ void __launch_bounds__(kThreads, 3) norm_tile_kernel(const NormProble
             }
         const Pair over = twice(first > 0 ? -1.0f / (float)first : 0.0f);
 #pragma unroll
-        for (int j = 0; j < H; ++j) {
+        for (int j = 0; j < H; ++j)
             k[j] = __shfl_sync(0xFFFFFFFFu, mul2(k[j], over), p.sub);   // minus k
-            s[j] = s[H + j] = 0;
-        }
+        // the sums about k, and once more about the mean where positions need it: those alone
+        // take the second walk's result, so that none depends on its neighbours
+        for (bool again = false;; again = true, turn ^= 1) {
+#pragma unroll
+            for (int j = 0; j < 2 * H; ++j)
+                s[j] = 0;
 #pragma unroll 4
-        for (int r = 0; r < p.n; ++r) {
-            chunk_to_pairs<T>(mine[r * kThreads], f);
+            for (int r = 0; r < p.n; ++r) {
+                chunk_to_pairs<T>(mine[r * kThreads], f);
 #pragma unroll
-            for (int j = 0; j < H; ++j) {
-                const Pair d = add2(f[j], k[j]);
-                s[j] = add2(s[j], d);
-                s[H + j] = fma2(d, d, s[H + j]);
+                for (int j = 0; j < H; ++j) {
+                    const Pair d = add2(f[j], k[j]);
+                    s[j] = add2(s[j], d);
+                    s[H + j] = fma2(d, d, s[H + j]);
+                }
             }
-        }
-        put_row_sums<H, -1, kTW>(s, part[threadIdx.x / 32], p.lpr_log, p.lane, p.sub);
-        if (p.lane < (1 << p.lpr_log))
+            put_row_sums<H, -1, kTW>(s, part[threadIdx.x / 32], p.lpr_log, p.lane, p.sub);
+            if (p.lane < (1 << p.lpr_log))
 #pragma unroll
-            for (int j = 0; j < H; ++j) {
-                const float2 u = halves(k[j]);
-                part_k[threadIdx.x / 32][p.sub * V + 2 * j] = -u.x;
-                part_k[threadIdx.x / 32][p.sub * V + 2 * j + 1] = -u.y;
-            }
-        __syncthreads();
-        {   // eight threads a position, one a warp's sums
+                for (int j = 0; j < H; ++j) {
+                    const float2 u = halves(k[j]);
+                    part_k[threadIdx.x / 32][p.sub * V + 2 * j] = -u.x;
+                    part_k[threadIdx.x / 32][p.sub * V + 2 * j + 1] = -u.y;
+                }
+            __syncthreads();
+            // eight threads a position, one a warp's sums
             static_assert(kThreads == 8 * kTW && kWarps == 8, "a thread for each warp and position");
             const int col = threadIdx.x / 8, g = threadIdx.x % 8;
-            Moments m = join8(Moments{part_k[g][col], part[g][col], part[g][kTW + col]}, count[g]);
+            const float s2 = part[g][kTW + col];
+            Moments m = join8(Moments{part_k[g][col], part[g][col], s2, s2}, count[g]);
             if (t.split > 1) {
                 cg::cluster_group cluster = cg::this_cluster();
                 if (g == 0)
@@ -427,18 +440,25 @@ __global__ void __launch_bounds__(kThreads, 3) norm_tile_kernel(const NormProble
                     m = *cluster.map_shared_rank(&own[turn][col], g);
                 m = join8(m, g < t.split ? (float)max(0, min(t.slice, (int)P.C - g * t.slice)) : 0.0f);
             }
-            if (g == 0) {
-                const float2 q = finish(m, t, P.eps);
+            bool cancelled = false;
+            if (g == 0 && col < min((int64_t)t.tw, left) && (!again || far)) {
+                const float2 q = finish(m, t, P.eps, &cancelled);
+                far = cancelled;
                 stat[col] = q;
-                if (rank == 0 && col < min((int64_t)t.tw, left)) {
+                if (rank == 0) {
                     if (P.mean)
                         P.mean[w.b * P.L + l0 + col] = -q.x;
                     if (P.rstd)
                         P.rstd[w.b * P.L + l0 + col] = q.y;
                 }
             }
+            // the same in every block of the cluster: they joined the same numbers
+            if (!__syncthreads_or(cancelled && !again))
+                break;
+#pragma unroll
+            for (int j = 0; j < H; ++j)
+                k[j] = pair(stat[p.sub * V + 2 * j].x, stat[p.sub * V + 2 * j + 1].x);
         }
-        __syncthreads();
         Pair rstd[H];
 #pragma unroll
         for (int j = 0; j < H; ++j) {
@@ -686,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormG
 // 192 KB).  That leaves the shared memory to the L1, needs no copies, takes any number of
 // channels, and lets 16 to 32 warps an SM hide the latencies.
 //
-// Measured (B200, 1965 MHz): the forward of [8, 512, 16000] bf16 62.8 us = 4.2 TB/s, 0.64 of
+// Measured (B200, 1965 MHz): the forward of [8, 512, 16000] bf16 63.9 us = 4.1 TB/s, 0.63 of
 // the copy bandwidth; the gradient from the checkpoint of [32, 1024, 8192] bf16 317 us = 4.3
 // TB/s, 0.65.  DRAM moves only what it must; the loads' latency is the limit (7 of 13 cycles
 // a warp between two instructions in the forward), and the gradient's 23 instructions a
@@ -699,12 +719,14 @@ constexpr int kStreamTW = 64;
 // 64.6, 8 rows and 16 warps 74.  Gradient: 8 rows and 16 warps 327 us, 4 rows and 24 warps 418.
 constexpr int kRows = 4, kGradRows = 8;
 
+// With the codes three blocks an SM: four leave too few registers (forward and gradient of
+// [8, 512, 16000] bf16 181 us, with three 175).
 template <class T, bool CK, int LPR_LOG>
-__global__ void __launch_bounds__(kThreads, 4) norm_stream_kernel(const NormProblem P,
+__global__ void __launch_bounds__(kThreads, CK ? 3 : 4) norm_stream_kernel(const NormProblem P,
                                                                   const Tiling t) {
     constexpr int V = Vec<T>::V, H = Vec<T>::H;
     __shared__ __align__(8) float part[kWarps][2 * kStreamTW], part_k[kWarps][kStreamTW], count[kWarps];
-    __shared__ Moments own[kStreamTW];         // of the block's rows (cluster)
+    __shared__ Moments own[2][kStreamTW];      // of the block's rows (cluster), a walk's each
     __shared__ float2 stat[kStreamTW];         // (-mean, rstd)
     const int rank = t.split > 1 ? blockIdx.x % t.split : 0;
     const Walk w(t, t.split > 1 ? blockIdx.x / t.split : blockIdx.x);
@@ -738,10 +760,8 @@ __global__ void __launch_bounds__(kThreads, 4) norm_stream_kernel(const NormProb
         }
     const Pair over = twice(first > 0 ? -1.0f / (float)first : 0.0f);
 #pragma unroll
-    for (int j = 0; j < H; ++j) {
+    for (int j = 0; j < H; ++j)
         k[j] = __shfl_sync(0xFFFFFFFFu, mul2(k[j], over), p.sub);   // minus k
-        s[j] = s[H + j] = 0;
-    }
     auto add_row = [&](const uint4 &u) {
         chunk_to_pairs<T>(u, f);
 #pragma unroll
@@ -751,60 +771,78 @@ __global__ void __launch_bounds__(kThreads, 4) norm_stream_kernel(const NormProb
             s[H + j] = fma2(d, d, s[H + j]);
         }
     };
-    const T *x = x0;
-    int r = 0;
-    for (; r + kRows <= p.n; r += kRows) {
-        uint4 u[kRows];
+    uint32_t far = 0;                          // bit i: this thread's i-th position, below
+    // the sums about k, and once more about the mean where positions need it: those alone take
+    // the second walk's result, so that none depends on its neighbours
+    for (int again = 0;; again = 1) {
 #pragma unroll
-        for (int q = 0; q < kRows; ++q, x += x_hop)
-            u[q] = chunk(x);
+        for (int j = 0; j < 2 * H; ++j)
+            s[j] = 0;
+        const T *x = x0;
+        int r = 0;
+        for (; r + kRows <= p.n; r += kRows) {
+            uint4 u[kRows];
 #pragma unroll
-        for (int q = 0; q < kRows; ++q)
-            add_row(u[q]);
-    }
-    for (; r < p.n; ++r, x += x_hop)
-        add_row(chunk(x));
-    put_row_sums<H, LPR_LOG, kStreamTW>(s, part[threadIdx.x / 32], p.lpr_log, p.lane, p.sub);
-    if (p.lane < (1 << p.lpr_log))
+            for (int q = 0; q < kRows; ++q, x += x_hop)
+                u[q] = chunk(x);
 #pragma unroll
-        for (int j = 0; j < H; ++j) {
-            const float2 u = halves(k[j]);
-            part_k[threadIdx.x / 32][p.sub * V + 2 * j] = -u.x;
-            part_k[threadIdx.x / 32][p.sub * V + 2 * j + 1] = -u.y;
+            for (int q = 0; q < kRows; ++q)
+                add_row(u[q]);
         }
-    __syncthreads();
-    // eight threads a position, one a warp's sums
-    for (int c = threadIdx.x / 8; c < t.tw; c += kThreads / 8) {
-        const int g = threadIdx.x % 8;
-        const Moments m = join8(Moments{part_k[g][c], part[g][c], part[g][kStreamTW + c]}, count[g]);
-        if (g == 0)
-            own[c] = m;
-    }
-    if (t.split > 1)
-        cg::this_cluster().sync();
-    else
+        for (; r < p.n; ++r, x += x_hop)
+            add_row(chunk(x));
+        put_row_sums<H, LPR_LOG, kStreamTW>(s, part[threadIdx.x / 32], p.lpr_log, p.lane, p.sub);
+        if (p.lane < (1 << p.lpr_log))
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                const float2 u = halves(k[j]);
+                part_k[threadIdx.x / 32][p.sub * V + 2 * j] = -u.x;
+                part_k[threadIdx.x / 32][p.sub * V + 2 * j + 1] = -u.y;
+            }
         __syncthreads();
-    for (int c = threadIdx.x / 8; c < t.tw; c += kThreads / 8) {
-        const int g = threadIdx.x % 8;
-        Moments m = own[c];
-        if (t.split > 1) {
-            static_assert(kMaxSplit == 8, "a thread for each block");
-            if (g < t.split)
-                m = *cg::this_cluster().map_shared_rank(&own[c], g);
-            m = join8(m, g < t.split ? (float)max(0, min(t.slice, (int)P.C - g * t.slice)) : 0.0f);
+        // eight threads a position, one a warp's sums
+        for (int c = threadIdx.x / 8; c < t.tw; c += kThreads / 8) {
+            const int g = threadIdx.x % 8;
+            const float s2 = part[g][kStreamTW + c];
+            const Moments m = join8(Moments{part_k[g][c], part[g][c], s2, s2}, count[g]);
+            if (g == 0)
+                own[again][c] = m;
         }
-        if (g == 0) {
-            const float2 q = finish(m, t, P.eps);
-            stat[c] = q;
-            if (rank == 0 && c < left) {
-                if (P.mean)
-                    P.mean[w.b * P.L + l0 + c] = -q.x;
-                if (P.rstd)
-                    P.rstd[w.b * P.L + l0 + c] = q.y;
+        if (t.split > 1)
+            cg::this_cluster().sync();
+        else
+            __syncthreads();
+        uint32_t cancelled = 0, bit = 1;
+        for (int c = threadIdx.x / 8; c < t.tw; c += kThreads / 8, bit <<= 1) {
+            const int g = threadIdx.x % 8;
+            Moments m = own[again][c];
+            if (t.split > 1) {
+                static_assert(kMaxSplit == 8, "a thread for each block");
+                if (g < t.split)
+                    m = *cg::this_cluster().map_shared_rank(&own[again][c], g);
+                m = join8(m, g < t.split ? (float)max(0, min(t.slice, (int)P.C - g * t.slice)) : 0.0f);
+            }
+            if (g == 0 && c < left && (!again || (far & bit))) {
+                bool more;
+                const float2 q = finish(m, t, P.eps, &more);
+                cancelled |= more ? bit : 0u;
+                stat[c] = q;
+                if (rank == 0) {
+                    if (P.mean)
+                        P.mean[w.b * P.L + l0 + c] = -q.x;
+                    if (P.rstd)
+                        P.rstd[w.b * P.L + l0 + c] = q.y;
+                }
             }
         }
+        far = cancelled;
+        // the same in every block of the cluster: they joined the same numbers
+        if (!__syncthreads_or(!again && cancelled))
+            break;
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+            k[j] = pair(stat[p.sub * V + 2 * j].x, stat[p.sub * V + 2 * j + 1].x);
     }
-    __syncthreads();
     Pair rstd[H];
 #pragma unroll
     for (int j = 0; j < H; ++j) {
@@ -862,8 +900,8 @@ __global__ void __launch_bounds__(kThreads, 4) norm_stream_kernel(const NormProb
             scale += scale_hop;
         }
     };
-    x = x0;
-    r = 0;
+    const T *x = x0;
+    int r = 0;
     const int full = CK ? __shfl_sync(0xFFFFFFFFu, p.n, 31) : p.n;   // the warp's smallest
     for (; r + kRows <= full; r += kRows) {
         uint4 u[kRows];

@@ -425,11 +425,14 @@ const char *dcn1d_packed_forward_kernel_name(
  *   codes, scales  the 8-bit checkpoint of v (see dcn1d_checkpoint_pack), both or NULL
  *
  * L == 1 normalises rows of C contiguous values (single tokens).  Arithmetic and
- * statistics are fp32 (the variance is taken about the mean, in a second pass over values
- * held on chip or read again); y is rounded once.  A position that holds a NaN or an
- * infinity gives NaN at that position only; in the checkpoint it marks its blocks.  x is
- * read twice: y at x's address is DCN1D_ERR_ARG.  One launch, no scratch memory.  Sizes: B * L < 2^31 and C < 2^31; the number of elements
- * may pass 2^31.
+ * statistics are fp32: the variance is a sum of squares about the mean or about values near
+ * it (a position where those are too far takes its sums again about the mean), so large
+ * means and outlying channels cost it at most three times the roundings of a sum about the
+ * mean.  y is rounded once.  The codes are those of the fp32 v: another order of the same
+ * operations may move a value next to half a step to the next code.  A position that holds a
+ * NaN or an infinity gives NaN at that position only; in the checkpoint it marks its blocks.
+ * x is read more than once: y at x's address is DCN1D_ERR_ARG.  One launch, no scratch
+ * memory.  Sizes: B * L < 2^31 and C < 2^31; the number of elements may pass 2^31.
  */
 int dcn1d_layer_norm_forward(const dcn1d_tensor *x, const dcn1d_tensor *gamma,
                              const dcn1d_tensor *beta, float eps, dcn1d_tensor *y,
