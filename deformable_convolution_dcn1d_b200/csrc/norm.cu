@@ -29,6 +29,7 @@
 #include <cooperative_groups.h>
 
 #include "checkpoint.cuh"
+#include "norm_index.h"
 #include "pairs.cuh"
 #include "sm100.cuh"
 
@@ -39,6 +40,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+static_assert(kAnyThreads == kThreads && kCkBlock == 32, "norm_index.h");
 constexpr int kTW = 32;                        // positions of a tile, at most; a block of codes
 constexpr int kMaxSplit = 8;                   // blocks of a portable cluster
 
@@ -1434,44 +1436,41 @@ __device__ __forceinline__ float sum_over_rows(float v, int TL, float (*part)[32
 template <class T>
 __global__ void __launch_bounds__(kThreads) norm_any_kernel(const NormProblem P, int TL) {
     __shared__ float part[kWarps][32];
-    const int64_t tiles = (P.L + TL - 1) / TL;
-    const int64_t b = blockIdx.x / tiles, l0 = (blockIdx.x - b * tiles) * TL;
+    const AnyIndex at(P.C, P.L, TL);
+    const int64_t b = at.b_of(blockIdx.x), l = at.l_of(blockIdx.x, threadIdx.x);
     const int lane = threadIdx.x & 31, col = lane & (TL - 1);
-    const int rows = kThreads / TL, row0 = threadIdx.x / TL;
-    const int64_t l = l0 + col;
+    const int rows = at.rows(), row0 = threadIdx.x / TL;
     const bool in = l < P.L;
-    const T *x = static_cast<const T *>(P.x) + b * P.C * P.L + l;
+    const T *x = static_cast<const T *>(P.x);
     float s = 0.0f;
     for (int64_t c = row0; c < P.C; c += rows)
-        s += in ? ld_f32(x + c * P.L) : 0.0f;
+        s += in ? ld_f32(x + at.value(b, c, l)) : 0.0f;
     const float mean = sum_over_rows(s, TL, part) / (float)P.C;
     s = 0.0f;
     for (int64_t c = row0; c < P.C; c += rows) {
-        const float d = in ? ld_f32(x + c * P.L) - mean : 0.0f;
+        const float d = in ? ld_f32(x + at.value(b, c, l)) - mean : 0.0f;
         s = fmaf(d, d, s);
     }
     const float rstd = 1.0f / sqrtf(sum_over_rows(s, TL, part) / (float)P.C + P.eps);
     if (in && row0 == 0) {
         if (P.mean)
-            P.mean[b * P.L + l] = mean;
+            P.mean[at.stat(b, l)] = mean;
         if (P.rstd)
-            P.rstd[b * P.L + l] = rstd;
+            P.rstd[at.stat(b, l)] = rstd;
     }
-    T *y = static_cast<T *>(P.y) + b * P.C * P.L + l;
     const bool along_c = P.L == 1;
-    const int64_t nb = ck_blocks(along_c ? P.C : P.L);
     // whole warps walk the rows together: the block maximum below is a warp reduction
     for (int64_t c0 = 0; c0 < P.C; c0 += rows) {
         const int64_t c = c0 + row0;
         const bool ok = in && c < P.C;
-        const float v = ok ? (ld_f32(x + c * P.L) - mean) * rstd : 0.0f;
+        const float v = ok ? (ld_f32(x + at.value(b, c, l)) - mean) * rstd : 0.0f;
         if (ok) {
             float o = v;
             if (P.gamma)
                 o = o * ld_f32(static_cast<const T *>(P.gamma) + c);
             if (P.beta)
                 o = o + ld_f32(static_cast<const T *>(P.beta) + c);
-            y[c * P.L] = from_f32<T>(o);
+            static_cast<T *>(P.y)[at.value(b, c, l)] = from_f32<T>(o);
         }
         if (P.codes) {
             uint32_t m = ck_abs_bits(v);
@@ -1479,10 +1478,9 @@ __global__ void __launch_bounds__(kThreads) norm_any_kernel(const NormProblem P,
                 m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             const uint32_t e = ck_scale(m, ck_top<float>());
             if (ok) {
-                P.codes[(b * P.C + c) * P.L + l] = (int8_t)ck_code(v, ck_inverse(e));
+                P.codes[at.value(b, c, l)] = (int8_t)ck_code(v, ck_inverse(e));
                 if (along_c ? lane == 0 : col == 0)
-                    P.scales[along_c ? b * nb + c / kCkBlock
-                                     : (b * P.C + c) * nb + l / kCkBlock] = (uint8_t)e;
+                    P.scales[at.step(b, c, l)] = (uint8_t)e;
             }
         }
     }
@@ -1495,37 +1493,27 @@ template <class T, bool CK>
 __global__ void __launch_bounds__(kThreads) norm_grad_any_kernel(const NormGrad P, int TL,
                                                                  int64_t ntiles, float *part_g) {
     __shared__ float part[kWarps][32];
-    const int64_t tiles = (P.L + TL - 1) / TL;
+    const AnyIndex at(P.C, P.L, TL);
     const int lane = threadIdx.x & 31, col = lane & (TL - 1);
-    const int rows = kThreads / TL, row0 = threadIdx.x / TL;
-    const bool along_c = P.L == 1;
-    const int64_t nb = ck_blocks(along_c ? P.C : P.L);
-    const int64_t total = P.B * P.C * P.L;
-    // every access is checked: free next to the rest, in a kernel for sizes that are rarely run
-    auto inside = [&](int64_t at) { return at >= 0 && at < total; };
-    float *pg = part_g ? part_g + (int64_t)blockIdx.x * 2 * P.C : nullptr;
+    const int rows = at.rows(), row0 = threadIdx.x / TL;
+    float *pg = part_g ? part_g + at.part(blockIdx.x) : nullptr;
     for (int64_t tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
-        const int64_t b = tile / tiles, l = (tile - b * tiles) * TL + col;
+        const int64_t b = at.b_of(tile), l = at.l_of(tile, threadIdx.x);
         const bool in = l < P.L;
-        const float rstd = in ? P.rstd[b * P.L + l] : 0.0f;
-        const float mean = !CK && in ? P.mean[b * P.L + l] : 0.0f;
+        const float rstd = in ? P.rstd[at.stat(b, l)] : 0.0f;
+        const float mean = !CK && in ? P.mean[at.stat(b, l)] : 0.0f;
         auto value = [&](int64_t c) {
-            const int64_t at = (b * P.C + c) * P.L + l;
-            if (!inside(at))
-                return 0.0f;
             if (CK)
-                return (float)P.codes[at] *
-                       ck_step(P.scales[along_c ? b * nb + c / kCkBlock
-                                                : (b * P.C + c) * nb + l / kCkBlock]);
-            return (ld_f32(static_cast<const T *>(P.x) + at) - mean) * rstd;
+                return (float)P.codes[at.value(b, c, l)] * ck_step(P.scales[at.step(b, c, l)]);
+            return (ld_f32(static_cast<const T *>(P.x) + at.value(b, c, l)) - mean) * rstd;
         };
         const T *gy = static_cast<const T *>(P.gy);
         float a = 0.0f, q = 0.0f;
         for (int64_t c0 = 0; c0 < P.C; c0 += rows) {
             const int64_t c = c0 + row0;
             float g = 0.0f, v = 0.0f;
-            if (in && c < P.C && inside((b * P.C + c) * P.L + l)) {
-                g = ld_f32(gy + (b * P.C + c) * P.L + l);
+            if (in && c < P.C) {
+                g = ld_f32(gy + at.value(b, c, l));
                 v = value(c);
                 const float d = P.gamma ? g * ld_f32(static_cast<const T *>(P.gamma) + c) : g;
                 a += d;
@@ -1548,11 +1536,10 @@ __global__ void __launch_bounds__(kThreads) norm_grad_any_kernel(const NormGrad 
             const float A = sum_over_rows(a, TL, part) / (float)P.C;
             const float S = sum_over_rows(q, TL, part) / (float)P.C;
             if (in)
-                for (int64_t c = row0; c < P.C && inside((b * P.C + c) * P.L + l); c += rows) {
-                    const float g = ld_f32(gy + (b * P.C + c) * P.L + l);
+                for (int64_t c = row0; c < P.C; c += rows) {
+                    const float g = ld_f32(gy + at.value(b, c, l));
                     const float d = P.gamma ? g * ld_f32(static_cast<const T *>(P.gamma) + c) : g;
-                    static_cast<T *>(P.gx)[(b * P.C + c) * P.L + l] =
-                        from_f32<T>(rstd * (d - A - value(c) * S));
+                    static_cast<T *>(P.gx)[at.value(b, c, l)] = from_f32<T>(rstd * (d - A - value(c) * S));
                 }
         }
     }
@@ -1590,13 +1577,6 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float *par
     T *out = i < C ? ggamma : gbeta;
     if (chain == 0 && i < 2 * C && out)
         out[i < C ? i : i - C] = from_f32<T>(s);
-}
-
-int lanes_along(int64_t L) {
-    int TL = 1;
-    while (TL < 32 && TL < L)
-        TL *= 2;
-    return TL;
 }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
