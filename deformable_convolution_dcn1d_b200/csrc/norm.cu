@@ -709,8 +709,9 @@ __global__ void __launch_bounds__(kThreads, 3) norm_grad_tile_kernel(const NormG
 // channels, and lets 16 to 32 warps an SM hide the latencies.
 //
 // Measured (B200, 1965 MHz): the forward of [8, 512, 16000] bf16 63.9 us = 4.1 TB/s, 0.63 of
-// the copy bandwidth; the gradient from the checkpoint of [32, 1024, 8192] bf16 317 us = 4.3
-// TB/s, 0.65.  DRAM moves only what it must; the loads' latency is the limit (7 of 13 cycles
+// the copy bandwidth (79 us where channels lie far out and the sums are taken twice); the
+// gradient from the checkpoint of [32, 1024, 8192] bf16 317 us = 4.3
+// TB/s, 0.65.  DRAM moves only what it must; the loads' latency is the limit (6 of 13 cycles
 // a warp between two instructions in the forward), and the gradient's 23 instructions a
 // value next to it.  Tiles staged in shared memory with the next one's copies under way took
 // 65 and 645 us (their exchange between warps is paid for half as many positions), a tile
