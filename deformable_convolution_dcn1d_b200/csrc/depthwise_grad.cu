@@ -28,10 +28,10 @@
 // they reach the sites they belong to, and a row too long for the bits q beside its sums.
 //
 // Measured (B200): [8, 512, 16000] bf16, 3 taps, 768 us for 1.11 GB = 1.45 TB/s, 0.22 of the
-// copy bandwidth; fp32 1186 us.  Bound by issue (84 % of the slots, 112 instructions a tap,
-// about a third of them the first walk's) and by the shared-memory pipe (76 %: the two
-// additions or maxima of a tap collide about 4 ways, as offsets scatter the lanes).  One unit
-// for a whole row took 450 us and lost what lies far below the row's largest; fp32 additions
+// copy bandwidth; fp32 1186 us.  Bound by issue (84 % of the slots, 112 instructions a tap
+// over both walks) and by the shared-memory pipe (76 %: the two additions or maxima of a tap
+// collide about 4 ways, as offsets scatter the lanes).  One unit for a whole row took 456 us
+// and 65 instructions, and lost what lies far below the row's largest; fp32 additions
 // run at 61 SM cycles a warp and tap where these take 51 (rows of 34000 to 37000, bf16).
 // 512 threads and at most 64 registers for K <= 4: two blocks an SM, so that one
 // unpacks or writes out while the other walks; more taps need the registers.
